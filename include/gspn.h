@@ -112,7 +112,9 @@ enum {
     GSPN_ERR_HIP = -9,    /* a HIP call failed; see gspn_last_error() */
     GSPN_ERR_PATH = -10,  /* unknown path, or the path (or the backward) cannot take this shape */
     GSPN_ERR_FLAGS = -11, /* unknown bit in flags (gspn_scan_fwd_ex, gspn_scan_bwd_ex, gspn_block_fwd) */
-    GSPN_ERR_SCRATCH = -12 /* the shape's workspace exceeds GSPN_NOALLOC_SCRATCH_BYTES (gspn_scan_fwd_noalloc) */
+    GSPN_ERR_SCRATCH = -12, /* the shape's workspace exceeds GSPN_NOALLOC_SCRATCH_BYTES (gspn_scan_fwd_noalloc) */
+    GSPN_ERR_STRIDE = -13, /* a row stride is negative, or rows of an output overlap (gspn_seq_*, gspn_adapter_add) */
+    GSPN_ERR_WORK = -14    /* the caller's workspace is missing or too small (gspn_seq_*, gspn_adapter_add) */
 };
 
 /* Flags of gspn_scan_fwd_ex and gspn_scan_bwd_ex. */
@@ -372,6 +374,161 @@ int gspn_block_fwd(const void *x, const void *w_in, const void *w_out, void *z, 
 /* Rows of gspn_block_fwd's w_in, 3*C_proxy + 3*popcount(dirs)*(C_proxy/ch_per_weight),
  * or a negative GSPN_ERR_* code for invalid arguments. */
 int64_t gspn_block_rows(int64_t C_proxy, uint32_t dirs, int32_t ch_per_weight);
+
+/*
+ * ---------------------------------------------------------------- sequences
+ * The recurrence along one axis: the causal form of the scan that a language
+ * model runs over tokens.  Where a line of the 2D scan couples each position
+ * to its three neighbours through row-stochastic taps, a token has one
+ * predecessor, and a sigmoid gate says how much of its state stays:
+ *
+ *   a_t = sigmoid(gate[t][k])                      k = d / ch_per_weight
+ *   h_t = a_t h_{t-1} + lam[t][d] x[t][d]          with lam
+ *   h_t = a_t h_{t-1} + (1 - a_t) x[t][d]          lam NULL (the gate shares
+ *                                                  itself out, w and 1 - w)
+ *   y[t][d] = u[t][d] h_t                          u NULL: y = h
+ *
+ * for every channel d of every sequence n, with h before the first token
+ * h0[n][d] (h0 NULL: 0), and h_last[n][d] the state behind the last (h0[n]
+ * for a sequence of no tokens).
+ *
+ * Tokens lie packed, one row of D channels each: sequence n holds the rows
+ * offsets[n] .. offsets[n+1] - 1 (offsets: N + 1 ascending int32 on the
+ * device, offsets[0] = 0, offsets[N] <= T; sequences may be empty).  offsets
+ * NULL: N sequences of T / N rows each.  Rows from offsets[N] on belong to
+ * no sequence: their inputs are never used and their outputs are left as
+ * they were, or set to zero with GSPN_SEQ_ZERO_TAIL.  Values never pass from
+ * one sequence to another, NaN and Inf included.  The contents of offsets
+ * are not checked; whatever they hold, no access leaves the tensors and the
+ * call ends.
+ *
+ * Every x / gate / lam / u / y row starts `*_stride` elements after the one
+ * before it (so the four inputs may be column ranges of one projection's
+ * output; 0 repeats one row for every token), channels lie next to each
+ * other.  Pointers are aligned to their elements; rows whose pointers and
+ * strides are multiples of 4 bytes are read two channels at a time.
+ * Arithmetic is fp32; states are fp32 at every boundary (h0, h_last, states,
+ * the cache of gspn_seq_step), y and the gradients are rounded once to the
+ * I/O dtype.
+ *
+ * Errors as above: sizes, dtype, pointers, strides, overlaps of an output
+ * with anything else the call uses, and the workspace are checked on the
+ * host before anything is enqueued.  Calls enqueue on `stream`, allocate
+ * nothing and keep nothing; results are deterministic.  A workspace is the
+ * caller's, 16-byte aligned, needs no initial contents and serves one call
+ * at a time: calls that may overlap (two streams, two captured graphs that
+ * run side by side) need one each.
+ */
+
+/* Flags of gspn_seq and gspn_adapter. */
+enum {
+    GSPN_SEQ_ZERO_TAIL = 1 /* output rows behind the last sequence are set to zero */
+};
+
+typedef struct {
+    const void *x, *gate;       /* [T][D], [T][D / ch_per_weight] */
+    const void *lam, *u;        /* [T][D], each may be NULL */
+    const int32_t *offsets;     /* [N + 1], may be NULL */
+    const float *h0;            /* [N][D], may be NULL */
+    void *y;                    /* [T][D] output (gspn_seq_bwd: not used) */
+    float *h_last;              /* [N][D] output, may be NULL (gspn_seq_bwd: not used) */
+    float *states;              /* [gspn_seq_states_rows(T, N)][D]: gspn_seq_fwd writes what gspn_seq_bwd
+                                   reads, NULL to write none */
+    void *work;                 /* gspn_seq_workspace bytes, NULL where that is 0 */
+    int64_t work_bytes;
+    int64_t T, D, N;            /* T >= 0, D and N >= 1 */
+    int64_t x_stride, gate_stride, lam_stride, u_stride, y_stride;
+    int32_t ch_per_weight;      /* channels that share a gate, divides D */
+    int32_t dtype;              /* gspn_dtype of x, gate, lam, u, y and of the gradients */
+    uint32_t flags;             /* GSPN_SEQ_ZERO_TAIL or 0 */
+} gspn_seq;
+
+/* Forward.  Returns GSPN_OK or a negative GSPN_ERR_* code. */
+int gspn_seq_fwd(const gspn_seq *seq, hipStream_t stream);
+
+/*
+ * Backward of gspn_seq_fwd: the exact vector-Jacobian product.  With
+ * S_t = u_t gy_t, plus gh_last[n] at the last token, and G the adjoint state:
+ *   G_t = S_t + a_{t+1} G_{t+1},   gh0[n] = a_first G_first  (gh_last[n] for
+ *   an empty sequence),   gu_t = gy_t h_t
+ *   with lam:  gx = lam G, glam = x G,
+ *              ggate[t][k] = a (1 - a) sum over the set's channels of G h_{t-1}
+ *   lam NULL:  gx = (1 - a) G,
+ *              ggate[t][k] = a (1 - a) sum of G (h_{t-1} - x)
+ * `states` is what gspn_seq_fwd wrote for the same inputs; y and h_last of
+ * `seq` are not used.  gy NULL stands for zeros, gh_last NULL too.  Any
+ * gradient may be NULL and is then not written; glam and gu need lam and u.
+ */
+typedef struct {
+    const void *gy;             /* [T][D], may be NULL */
+    const float *gh_last;       /* [N][D], may be NULL */
+    void *gx, *ggate, *glam, *gu;
+    float *gh0;                 /* [N][D] */
+    int64_t gy_stride, gx_stride, ggate_stride, glam_stride, gu_stride;
+} gspn_seq_grad;
+
+int gspn_seq_bwd(const gspn_seq *seq, const gspn_seq_grad *grad, hipStream_t stream);
+
+/* Bytes of workspace of gspn_seq_fwd (backward = 0) or gspn_seq_bwd (1) for
+ * the sizes, offsets (NULL or not), ch_per_weight, dtype of *seq; its other
+ * pointers are not used.  A negative code for invalid sizes. */
+int64_t gspn_seq_workspace(const gspn_seq *seq, int32_t backward);
+
+/* Rows of `states`, or a negative code for invalid sizes. */
+int64_t gspn_seq_states_rows(int64_t T, int64_t N);
+
+/*
+ * One token for each of N requests, whose states live in a cache:
+ *   state[s] = a state[s] + lam x   (or (1 - a) x),   y = u state[s],
+ * s = slots[row] (slots NULL: row), in place.  A row whose slot is outside
+ * [0, S) is skipped: it changes no state and its y is left as it was (a row of
+ * padding takes slot -1).  Rows of the same slot are tokens of one request:
+ * they are taken one after the other, in the order of their rows.
+ */
+typedef struct {
+    const void *x, *gate, *lam, *u; /* [N][D] ([N][D / ch_per_weight]); lam and u may be NULL */
+    const int32_t *slots;           /* [N], may be NULL (then N <= S) */
+    float *state;                   /* [S][D] */
+    void *y;                        /* [N][D] */
+    int64_t N, S, D;                /* N >= 0, S and D >= 1 */
+    int64_t x_stride, gate_stride, lam_stride, u_stride, y_stride;
+    int32_t ch_per_weight, dtype;
+} gspn_seq_token;
+
+int gspn_seq_step(const gspn_seq_token *tok, hipStream_t stream);
+
+/*
+ * Low-rank adapters of many requests, added to what a shared projection gave:
+ *   out[t] = base[t] + scale[i] * b[i] (a[i] x[t]),   i = ids[n]
+ * for every row t of request n (rows and requests as for gspn_seq, offsets
+ * NULL: T / N rows each).  ids outside [0, R) stand for no adapter: out[t] =
+ * base[t].  scale NULL: 1.  out may be base itself (same pointer and stride)
+ * and overlaps nothing else.  Rows behind the last request: left as they
+ * were, zero with GSPN_SEQ_ZERO_TAIL.  Both products are summed in fp32 and
+ * out is rounded once.  1 <= r <= GSPN_MAX_RANK.  Workspace:
+ * gspn_adapter_workspace bytes.
+ */
+#define GSPN_MAX_RANK 256
+
+typedef struct {
+    const void *base, *x;       /* [T][M], [T][K] */
+    const void *a, *b;          /* [R][r][K], [R][M][r], contiguous */
+    const float *scale;         /* [R], may be NULL */
+    const int32_t *ids;         /* [N] */
+    const int32_t *offsets;     /* [N + 1], may be NULL */
+    void *out;                  /* [T][M] */
+    void *work;
+    int64_t work_bytes;
+    int64_t T, K, M, N, R, r;
+    int64_t base_stride, x_stride, out_stride;
+    int32_t dtype;              /* of base, x, a, b and out */
+    uint32_t flags;
+} gspn_adapter;
+
+int gspn_adapter_add(const gspn_adapter *ad, hipStream_t stream);
+
+/* Bytes of workspace of gspn_adapter_add for the sizes of *ad, or a negative code. */
+int64_t gspn_adapter_workspace(const gspn_adapter *ad);
 
 /* GSPN_OK if gspn_scan_bwd can run these sizes, GSPN_ERR_PATH if the shape is
  * outside its kernels, or another negative code for invalid sizes. */

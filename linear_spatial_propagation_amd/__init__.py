@@ -6,6 +6,9 @@
     ys = scan_fwd_batched([dict(x=..., w_raw=..., lam=..., u=...), ...])   # one launch
     y = gspn_scan(x, w_raw, lam, u, ...)   # differentiable: autograd runs scan_bwd
     z = block_fwd(x, w_in, w_out, ...)     # compressed block: projections around the scan
+    y, h_last = seq_scan(x, gate, lam=lam, u=u, offsets=offsets)   # the recurrence over tokens, differentiable
+    y = seq_step(x, gate, state, slots=slots)   # one token of each request on a cache of states
+    out = adapter_add(base, x, a, b, ids, offsets=offsets)   # low-rank adapters of many requests
 
 computes the 4-direction line recurrence of the Generalized Spatial
 Propagation Network with hand-written HIP kernels (libgspn.so, C ABI in
@@ -15,16 +18,21 @@ this wrapper only checks tensors and passes pointers.
 Tensors (same dtype, float32 or bfloat16, contiguous, on one GPU):
   x, lam, u : [B, C, H, W]
   w_raw     : [popcount(dirs), B, C // ch_per_weight, 3, H, W]
+The sequence operators and the adapters lay out theirs as sequence.py and
+adapters.py say.
 """
 from __future__ import annotations
 
 from . import _lib
 from ._lib import (DIR_ALL, DIR_BT, DIR_LR, DIR_RL, DIR_TB, PATH_AUTO, PATH_FUSED, PATH_GENERAL, PATH_SLICE,
                    GspnError, load, select_path)
+from .adapters import adapter_add
+from .sequence import seq_scan, seq_scan_bwd, seq_scan_fwd, seq_step
 
 __all__ = ["scan_fwd", "scan_bwd", "scan_fwd_dirs", "scan_bwd_dirs", "scan_fwd_batched", "gspn_scan", "block_fwd",
-           "block_rows", "select_path", "load", "GspnError", "DIR_TB", "DIR_BT", "DIR_LR", "DIR_RL",
-           "DIR_ALL", "PATH_AUTO", "PATH_FUSED", "PATH_GENERAL", "PATH_SLICE"]
+           "block_rows", "seq_scan", "seq_scan_fwd", "seq_scan_bwd", "seq_step", "adapter_add", "select_path", "load",
+           "GspnError", "DIR_TB", "DIR_BT", "DIR_LR", "DIR_RL", "DIR_ALL", "PATH_AUTO", "PATH_FUSED", "PATH_GENERAL",
+           "PATH_SLICE"]
 
 
 def _dtype_code(t):

@@ -26,6 +26,8 @@ MAX_BATCH = 32
 NOALLOC_SCRATCH_BYTES = 64 << 20
 BLOCK_RMSNORM = 1
 ERR_SCRATCH = -12
+SEQ_ZERO_TAIL = 1
+MAX_RANK = 256
 
 
 class Problem(ctypes.Structure):
@@ -35,9 +37,43 @@ class Problem(ctypes.Structure):
                 ("C", ctypes.c_int64), ("H", ctypes.c_int64), ("W", ctypes.c_int64),
                 ("dirs", ctypes.c_uint32), ("groups", ctypes.c_int32), ("ch_per_weight", ctypes.c_int32)]
 
+class Seq(ctypes.Structure):
+    """gspn_seq of include/gspn.h."""
+    _fields_ = ([(nm, ctypes.c_void_p) for nm in ("x", "gate", "lam", "u", "offsets", "h0", "y", "h_last", "states",
+                                                  "work")]
+                + [(nm, ctypes.c_int64) for nm in ("work_bytes", "T", "D", "N", "x_stride", "gate_stride",
+                                                   "lam_stride", "u_stride", "y_stride")]
+                + [("ch_per_weight", ctypes.c_int32), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)])
+
+
+class SeqGrad(ctypes.Structure):
+    """gspn_seq_grad of include/gspn.h."""
+    _fields_ = ([(nm, ctypes.c_void_p) for nm in ("gy", "gh_last", "gx", "ggate", "glam", "gu", "gh0")]
+                + [(nm, ctypes.c_int64) for nm in ("gy_stride", "gx_stride", "ggate_stride", "glam_stride",
+                                                   "gu_stride")])
+
+
+class SeqToken(ctypes.Structure):
+    """gspn_seq_token of include/gspn.h."""
+    _fields_ = ([(nm, ctypes.c_void_p) for nm in ("x", "gate", "lam", "u", "slots", "state", "y")]
+                + [(nm, ctypes.c_int64) for nm in ("N", "S", "D", "x_stride", "gate_stride", "lam_stride",
+                                                   "u_stride", "y_stride")]
+                + [("ch_per_weight", ctypes.c_int32), ("dtype", ctypes.c_int32)])
+
+
+class Adapter(ctypes.Structure):
+    """gspn_adapter of include/gspn.h."""
+    _fields_ = ([(nm, ctypes.c_void_p) for nm in ("base", "x", "a", "b", "scale", "ids", "offsets", "out", "work")]
+                + [(nm, ctypes.c_int64) for nm in ("work_bytes", "T", "K", "M", "N", "R", "r", "base_stride",
+                                                   "x_stride", "out_stride")]
+                + [("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)])
+
+
 EXPORTED = ("gspn_scan_fwd", "gspn_scan_fwd_noalloc", "gspn_scan_fwd_path", "gspn_scan_fwd_ex", "gspn_scan_fwd_batched",
             "gspn_select_path", "gspn_scan_bwd",
             "gspn_scan_bwd_path", "gspn_scan_bwd_ex", "gspn_bwd_supported", "gspn_block_fwd", "gspn_block_rows",
+            "gspn_seq_fwd", "gspn_seq_bwd", "gspn_seq_step", "gspn_seq_workspace", "gspn_seq_states_rows",
+            "gspn_adapter_add", "gspn_adapter_workspace",
             "gspn_status_string", "gspn_last_error", "gspn_version")
 
 _lock = threading.Lock()
@@ -86,6 +122,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.gspn_block_fwd.restype = ctypes.c_int
         lib.gspn_block_rows.argtypes = [i64, u32, i32]
         lib.gspn_block_rows.restype = ctypes.c_int64
+        lib.gspn_seq_fwd.argtypes = [ctypes.POINTER(Seq), vp]
+        lib.gspn_seq_bwd.argtypes = [ctypes.POINTER(Seq), ctypes.POINTER(SeqGrad), vp]
+        lib.gspn_seq_step.argtypes = [ctypes.POINTER(SeqToken), vp]
+        lib.gspn_seq_workspace.argtypes = [ctypes.POINTER(Seq), i32]
+        lib.gspn_seq_states_rows.argtypes = [i64, i64]
+        lib.gspn_adapter_add.argtypes = [ctypes.POINTER(Adapter), vp]
+        lib.gspn_adapter_workspace.argtypes = [ctypes.POINTER(Adapter)]
+        for name in ("gspn_seq_fwd", "gspn_seq_bwd", "gspn_seq_step", "gspn_adapter_add"):
+            getattr(lib, name).restype = ctypes.c_int
+        for name in ("gspn_seq_workspace", "gspn_seq_states_rows", "gspn_adapter_workspace"):
+            getattr(lib, name).restype = ctypes.c_int64
         lib.gspn_status_string.argtypes = [ctypes.c_int]
         lib.gspn_status_string.restype = ctypes.c_char_p
         lib.gspn_last_error.argtypes = []

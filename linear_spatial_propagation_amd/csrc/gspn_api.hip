@@ -5,6 +5,7 @@
 
 #include <rocblas/rocblas.h>
 
+#include <algorithm>
 #include <mutex>
 #include <stdint.h>
 #include <stdio.h>
@@ -74,6 +75,8 @@ const char* gspn_status_string(int status) {
         case GSPN_ERR_PATH: return "GSPN_ERR_PATH: unknown path, or the path cannot run this shape";
         case GSPN_ERR_FLAGS: return "GSPN_ERR_FLAGS: unknown bit in flags";
         case GSPN_ERR_SCRATCH: return "GSPN_ERR_SCRATCH: the shape's workspace exceeds the static scratch";
+        case GSPN_ERR_STRIDE: return "GSPN_ERR_STRIDE: a row stride is negative, or rows of an output overlap";
+        case GSPN_ERR_WORK: return "GSPN_ERR_WORK: the workspace is missing or too small";
         default: return "unknown GSPN status";
     }
 }
@@ -561,6 +564,244 @@ int gspn_block_fwd(const void* x, const void* w_in, const void* w_out, void* z, 
     const hipError_t ef = hipFreeAsync(work, stream);
     if (rc != GSPN_OK) return rc;
     if (ef != hipSuccess) { set_error("hipFreeAsync(workspace)", ef); return GSPN_ERR_HIP; }
+    return GSPN_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- sequences
+namespace {
+
+// A tensor of a call: its extent in bytes is what overlap checks go by.
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+
+size_t rows_bytes(int64_t rows, int64_t stride, int64_t width, size_t es) {
+    return rows > 0 ? ((size_t)(rows - 1) * (size_t)stride + (size_t)width) * es : 0;
+}
+
+int check_dtype(int32_t dtype) { return dtype == GSPN_F32 || dtype == GSPN_BF16 ? GSPN_OK : GSPN_ERR_DTYPE; }
+
+// No output shares a byte with an input or another output (null spans and
+// empty ones share none).
+int check_apart(const Span* outs, int no, const Span* ins, int ni) {
+    for (int i = 0; i < no; ++i) {
+        if (!outs[i].p || !outs[i].bytes) continue;
+        for (int j = 0; j < ni; ++j)
+            if (ins[j].p && ins[j].bytes && overlaps(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes))
+                return GSPN_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (outs[j].p && outs[j].bytes && overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+                return GSPN_ERR_ALIAS;
+    }
+    return GSPN_OK;
+}
+
+bool unaligned(const void* p, size_t to) { return ((uintptr_t)p & (to - 1)) != 0; }
+
+constexpr int64_t kMaxTokens = 1LL << 30, kMaxWidth = 1LL << 20;
+
+int check_seq_sizes(int64_t T, int64_t D, int64_t N, int32_t cpw, int32_t dtype, bool packed) {
+    if (T < 0 || N < 1 || D < 1 || T > kMaxTokens || N > kMaxTokens || D > kMaxWidth) return GSPN_ERR_SHAPE;
+    if (!packed && T % N) return GSPN_ERR_SHAPE;
+    if (cpw < 1 || D % cpw) return GSPN_ERR_CPW;
+    if (check_dtype(dtype)) return GSPN_ERR_DTYPE;
+    // 32-bit launches: every kernel has at most one workgroup of 512 threads
+    // for 64 tokens, or a sequence's rest, and 64 channels
+    if ((T / 64 + N + 1) * ((D + 63) / 64) > (1LL << 22)) return GSPN_ERR_SHAPE;
+    return GSPN_OK;
+}
+
+// Sizes, strides and pointers of what both directions use.
+int check_seq(const gspn_seq& s, size_t es) {
+    const int rc = check_seq_sizes(s.T, s.D, s.N, s.ch_per_weight, s.dtype, s.offsets != nullptr);
+    if (rc) return rc;
+    if (s.flags & ~(uint32_t)GSPN_SEQ_ZERO_TAIL) return GSPN_ERR_FLAGS;
+    if (s.T > 0 && (!s.x || !s.gate)) return GSPN_ERR_NULL;
+    if (s.x_stride < 0 || s.gate_stride < 0 || s.lam_stride < 0 || s.u_stride < 0) return GSPN_ERR_STRIDE;
+    if (unaligned(s.x, es) || unaligned(s.gate, es) || unaligned(s.lam, es) || unaligned(s.u, es) ||
+        unaligned(s.offsets, 4) || unaligned(s.h0, 4) || unaligned(s.h_last, 4) || unaligned(s.states, 4) ||
+        unaligned(s.y, es) || unaligned(s.work, 16))
+        return GSPN_ERR_ALIGN;
+    return GSPN_OK;
+}
+
+bool rows_overlap(const void* p, int64_t rows, int64_t stride, int64_t width) {
+    return p && (stride < 0 || (rows > 1 && stride < width));
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t gspn_seq_states_rows(int64_t T, int64_t N) {
+    if (T < 0 || N < 1 || T > kMaxTokens || N > kMaxTokens) return GSPN_ERR_SHAPE;
+    return T / gspn::kSeqTile + N;
+}
+
+int64_t gspn_seq_workspace(const gspn_seq* seq, int32_t backward) {
+    if (!seq) return GSPN_ERR_NULL;
+    const int rc = check_seq_sizes(seq->T, seq->D, seq->N, seq->ch_per_weight, seq->dtype, seq->offsets != nullptr);
+    return rc ? rc : gspn::seq_workspace(*seq, backward != 0);
+}
+
+int gspn_seq_fwd(const gspn_seq* seq, hipStream_t stream) {
+    g_last_error[0] = '\0';
+    if (!seq) return GSPN_ERR_NULL;
+    const gspn_seq& s = *seq;
+    const size_t es = s.dtype == GSPN_BF16 ? 2 : 4;
+    const int rc = check_seq(s, es);
+    if (rc) return rc;
+    if (s.T > 0 && !s.y) return GSPN_ERR_NULL;
+    if (rows_overlap(s.y, s.T, s.y_stride, s.D)) return GSPN_ERR_STRIDE;
+    const size_t state = (size_t)s.N * s.D * 4;
+    const Span ins[] = {{s.x, rows_bytes(s.T, s.x_stride, s.D, es)},
+                        {s.gate, rows_bytes(s.T, s.gate_stride, s.D / s.ch_per_weight, es)},
+                        {s.lam, rows_bytes(s.T, s.lam_stride, s.D, es)},
+                        {s.u, rows_bytes(s.T, s.u_stride, s.D, es)},
+                        {s.offsets, ((size_t)s.N + 1) * 4},
+                        {s.h0, state}};
+    const int64_t need = gspn::seq_workspace(s, false);
+    const Span outs[] = {{s.y, rows_bytes(s.T, s.y_stride, s.D, es)},
+                         {s.h_last, state},
+                         {s.states, (size_t)gspn_seq_states_rows(s.T, s.N) * s.D * 4},
+                         {s.work, (size_t)need}};
+    if (check_apart(outs, 4, ins, 6)) return GSPN_ERR_ALIAS;
+    if (need > 0 && (!s.work || s.work_bytes < need)) return GSPN_ERR_WORK;
+    const hipError_t e = gspn::launch_seq_fwd(s, stream);
+    if (e != hipSuccess) { set_error("sequence kernel launch", e); return GSPN_ERR_HIP; }
+    return GSPN_OK;
+}
+
+int gspn_seq_bwd(const gspn_seq* seq, const gspn_seq_grad* grad, hipStream_t stream) {
+    g_last_error[0] = '\0';
+    if (!seq || !grad) return GSPN_ERR_NULL;
+    const gspn_seq& s = *seq;
+    const gspn_seq_grad& g = *grad;
+    const size_t es = s.dtype == GSPN_BF16 ? 2 : 4;
+    const int rc = check_seq(s, es);
+    if (rc) return rc;
+    if (!s.states || (g.glam && !s.lam) || (g.gu && !s.u)) return GSPN_ERR_NULL;
+    const int64_t Dk = s.D / s.ch_per_weight;
+    if (g.gy_stride < 0 || rows_overlap(g.gx, s.T, g.gx_stride, s.D) ||
+        rows_overlap(g.ggate, s.T, g.ggate_stride, Dk) || rows_overlap(g.glam, s.T, g.glam_stride, s.D) ||
+        rows_overlap(g.gu, s.T, g.gu_stride, s.D))
+        return GSPN_ERR_STRIDE;
+    if (unaligned(g.gy, es) || unaligned(g.gx, es) || unaligned(g.ggate, es) || unaligned(g.glam, es) ||
+        unaligned(g.gu, es) || unaligned(g.gh_last, 4) || unaligned(g.gh0, 4))
+        return GSPN_ERR_ALIGN;
+    const size_t state = (size_t)s.N * s.D * 4;
+    const Span ins[] = {{s.x, rows_bytes(s.T, s.x_stride, s.D, es)},
+                        {s.gate, rows_bytes(s.T, s.gate_stride, Dk, es)},
+                        {s.lam, rows_bytes(s.T, s.lam_stride, s.D, es)},
+                        {s.u, rows_bytes(s.T, s.u_stride, s.D, es)},
+                        {s.offsets, ((size_t)s.N + 1) * 4},
+                        {s.states, (size_t)gspn_seq_states_rows(s.T, s.N) * s.D * 4},
+                        {g.gy, rows_bytes(s.T, g.gy_stride, s.D, es)},
+                        {g.gh_last, state}};
+    const int64_t need = gspn::seq_workspace(s, true);
+    const Span outs[] = {{g.gx, rows_bytes(s.T, g.gx_stride, s.D, es)},
+                         {g.ggate, rows_bytes(s.T, g.ggate_stride, Dk, es)},
+                         {g.glam, rows_bytes(s.T, g.glam_stride, s.D, es)},
+                         {g.gu, rows_bytes(s.T, g.gu_stride, s.D, es)},
+                         {g.gh0, state},
+                         {s.work, (size_t)need}};
+    if (check_apart(outs, 6, ins, 8)) return GSPN_ERR_ALIAS;
+    if (need > 0 && (!s.work || s.work_bytes < need)) return GSPN_ERR_WORK;
+    const hipError_t e = gspn::launch_seq_bwd(s, g, stream);
+    if (e != hipSuccess) { set_error("sequence backward launch", e); return GSPN_ERR_HIP; }
+    return GSPN_OK;
+}
+
+int gspn_seq_step(const gspn_seq_token* tok, hipStream_t stream) {
+    g_last_error[0] = '\0';
+    if (!tok) return GSPN_ERR_NULL;
+    const gspn_seq_token& t = *tok;
+    if (t.N < 0 || t.S < 1 || t.D < 1 || t.N > (1LL << 20) || t.S > kMaxTokens || t.D > kMaxWidth)
+        return GSPN_ERR_SHAPE;
+    if (!t.slots && t.N > t.S) return GSPN_ERR_SHAPE;
+    if (t.N * ((t.D + 255) / 256) > (1LL << 22)) return GSPN_ERR_SHAPE;
+    if (t.ch_per_weight < 1 || t.D % t.ch_per_weight) return GSPN_ERR_CPW;
+    if (check_dtype(t.dtype)) return GSPN_ERR_DTYPE;
+    if (!t.state || (t.N > 0 && (!t.x || !t.gate || !t.y))) return GSPN_ERR_NULL;
+    if (t.x_stride < 0 || t.gate_stride < 0 || t.lam_stride < 0 || t.u_stride < 0 ||
+        rows_overlap(t.y, t.N, t.y_stride, t.D))
+        return GSPN_ERR_STRIDE;
+    const size_t es = t.dtype == GSPN_BF16 ? 2 : 4;
+    if (unaligned(t.x, es) || unaligned(t.gate, es) || unaligned(t.lam, es) || unaligned(t.u, es) ||
+        unaligned(t.y, es) || unaligned(t.slots, 4) || unaligned(t.state, 4))
+        return GSPN_ERR_ALIGN;
+    const Span ins[] = {{t.x, rows_bytes(t.N, t.x_stride, t.D, es)},
+                        {t.gate, rows_bytes(t.N, t.gate_stride, t.D / t.ch_per_weight, es)},
+                        {t.lam, rows_bytes(t.N, t.lam_stride, t.D, es)},
+                        {t.u, rows_bytes(t.N, t.u_stride, t.D, es)},
+                        {t.slots, (size_t)t.N * 4}};
+    const Span outs[] = {{t.y, rows_bytes(t.N, t.y_stride, t.D, es)}, {t.state, (size_t)t.S * t.D * 4}};
+    if (check_apart(outs, 2, ins, 5)) return GSPN_ERR_ALIAS;
+    if (t.N == 0) return GSPN_OK;
+    const hipError_t e = gspn::launch_seq_step(t, stream);
+    if (e != hipSuccess) { set_error("sequence step launch", e); return GSPN_ERR_HIP; }
+    return GSPN_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- adapters
+namespace {
+
+int check_adapter_sizes(const gspn_adapter& a) {
+    if (a.T < 0 || a.T > kMaxTokens || a.N < 1 || a.N > kMaxTokens || a.K < 1 || a.K > kMaxWidth || a.M < 1 ||
+        a.M > kMaxWidth || a.R < 1 || a.R > kMaxWidth || a.r < 1 || a.r > GSPN_MAX_RANK)
+        return GSPN_ERR_SHAPE;
+    if (!a.offsets && a.T % a.N) return GSPN_ERR_SHAPE;
+    if (check_dtype(a.dtype)) return GSPN_ERR_DTYPE;
+    // 32-bit launches: at most one workgroup for 16 tokens, or a request's
+    // rest, and 64 columns or ranks
+    if ((a.T / 16 + a.N + 1) * ((std::max(a.M, a.K) + 63) / 64) > (1LL << 23)) return GSPN_ERR_SHAPE;
+    return GSPN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t gspn_adapter_workspace(const gspn_adapter* ad) {
+    if (!ad) return GSPN_ERR_NULL;
+    const int rc = check_adapter_sizes(*ad);
+    return rc ? rc : gspn::adapter_workspace(*ad);
+}
+
+int gspn_adapter_add(const gspn_adapter* ad, hipStream_t stream) {
+    g_last_error[0] = '\0';
+    if (!ad) return GSPN_ERR_NULL;
+    const gspn_adapter& a = *ad;
+    const int rc = check_adapter_sizes(a);
+    if (rc) return rc;
+    if (a.flags & ~(uint32_t)GSPN_SEQ_ZERO_TAIL) return GSPN_ERR_FLAGS;
+    if (!a.a || !a.b || !a.ids || (a.T > 0 && (!a.base || !a.x || !a.out))) return GSPN_ERR_NULL;
+    if (a.base_stride < 0 || a.x_stride < 0 || rows_overlap(a.out, a.T, a.out_stride, a.M)) return GSPN_ERR_STRIDE;
+    const size_t es = a.dtype == GSPN_BF16 ? 2 : 4;
+    if (unaligned(a.base, es) || unaligned(a.x, es) || unaligned(a.a, es) || unaligned(a.b, es) ||
+        unaligned(a.out, es) || unaligned(a.scale, 4) || unaligned(a.ids, 4) || unaligned(a.offsets, 4) ||
+        unaligned(a.work, 16))
+        return GSPN_ERR_ALIGN;
+    const bool in_place = a.out == a.base && a.out_stride == a.base_stride;
+    const int64_t need = gspn::adapter_workspace(a);
+    const Span ins[] = {{a.x, rows_bytes(a.T, a.x_stride, a.K, es)},
+                        {a.a, (size_t)a.R * a.r * a.K * es},
+                        {a.b, (size_t)a.R * a.M * a.r * es},
+                        {a.scale, (size_t)a.R * 4},
+                        {a.ids, (size_t)a.N * 4},
+                        {a.offsets, ((size_t)a.N + 1) * 4},
+                        {in_place ? nullptr : a.base, rows_bytes(a.T, a.base_stride, a.M, es)}};
+    const Span outs[] = {{a.out, rows_bytes(a.T, a.out_stride, a.M, es)}, {a.work, (size_t)need}};
+    if (check_apart(outs, 2, ins, 7)) return GSPN_ERR_ALIAS;
+    if (need > 0 && (!a.work || a.work_bytes < need)) return GSPN_ERR_WORK;
+    if (a.T == 0) return GSPN_OK;
+    const hipError_t e = gspn::launch_adapter(a, stream);
+    if (e != hipSuccess) { set_error("adapter kernel launch", e); return GSPN_ERR_HIP; }
     return GSPN_OK;
 }
 

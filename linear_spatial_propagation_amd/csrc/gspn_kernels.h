@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/gspn.h"
+
 namespace gspn {
 
 // One validated call.  Sizes fit in int (checked by the C ABI layer).
@@ -87,5 +89,17 @@ hipError_t launch_slice(const ScanArgs& a, hipStream_t stream);
 // Per-line fallback: any H, W <= 4096.  `planes` is an fp32 workspace of
 // popcount(dirs) * B*C*H*W floats.
 hipError_t launch_general(const ScanArgs& a, float* planes, hipStream_t stream);
+
+// Sequences (gspn_seq.hip).  The arguments are validated; sizes as the C ABI
+// has them.  seq_workspace: bytes, for the forward or the backward.
+constexpr int kSeqTile = 64;   // tokens between two saved states
+int64_t seq_workspace(const gspn_seq& s, bool backward);
+hipError_t launch_seq_fwd(const gspn_seq& s, hipStream_t stream);
+hipError_t launch_seq_bwd(const gspn_seq& s, const gspn_seq_grad& g, hipStream_t stream);
+hipError_t launch_seq_step(const gspn_seq_token& t, hipStream_t stream);
+
+// Adapters of many requests (gspn_adapter.hip), arguments validated.
+int64_t adapter_workspace(const gspn_adapter& a);
+hipError_t launch_adapter(const gspn_adapter& a, hipStream_t stream);
 
 }  // namespace gspn
