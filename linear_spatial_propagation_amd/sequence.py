@@ -155,7 +155,7 @@ def seq_scan_fwd(x, gate, *, lam=None, u=None, offsets=None, h0=None, ch_per_wei
 
     y is shaped like x; h_last [N, D] float32 is each sequence's state behind
     its last token (h0's for a sequence of none).  return_states adds what
-    seq_scan_bwd needs: the states in front of every 64th token.
+    seq_scan_bwd needs: the state in front of every 128th token of a sequence.
     """
     import torch
     s = _sequence(x, gate, lam, u, offsets, h0, ch_per_weight)

@@ -125,7 +125,7 @@ def test_adapter_refuses(lib, kw, code):
 
 def test_sizes(lib):
     assert lib.gspn_seq_states_rows(0, 3) == 3
-    assert lib.gspn_seq_states_rows(130, 2) == 4
+    assert lib.gspn_seq_states_rows(130, 2) == 3
     assert lib.gspn_seq_states_rows(-1, 2) == SHAPE
     assert lib.gspn_seq_workspace(ctypes.byref(seq(N=0)), 0) == SHAPE
     assert lib.gspn_adapter_workspace(ctypes.byref(adapter(r=300))) == SHAPE
