@@ -608,9 +608,9 @@ int check_seq_sizes(int64_t T, int64_t D, int64_t N, int32_t cpw, int32_t dtype,
     if (!packed && T % N) return GSPN_ERR_SHAPE;
     if (cpw < 1 || D % cpw) return GSPN_ERR_CPW;
     if (check_dtype(dtype)) return GSPN_ERR_DTYPE;
-    // 32-bit launches: every kernel has at most one workgroup of 512 threads
-    // for 64 tokens, or a sequence's rest, and 64 channels
-    if ((T / 64 + N + 1) * ((D + 63) / 64) > (1LL << 22)) return GSPN_ERR_SHAPE;
+    // 32-bit launches: at most one workgroup of 512 threads for a tile of
+    // tokens, or a sequence's rest, and 64 channels
+    if ((T / gspn::kSeqTile + N + 1) * ((D + 63) / 64) > (1LL << 22)) return GSPN_ERR_SHAPE;
     return GSPN_OK;
 }
 
@@ -757,9 +757,9 @@ int check_adapter_sizes(const gspn_adapter& a) {
         return GSPN_ERR_SHAPE;
     if (!a.offsets && a.T % a.N) return GSPN_ERR_SHAPE;
     if (check_dtype(a.dtype)) return GSPN_ERR_DTYPE;
-    // 32-bit launches: at most one workgroup for 16 tokens, or a request's
-    // rest, and 64 columns or ranks
-    if ((a.T / 16 + a.N + 1) * ((std::max(a.M, a.K) + 63) / 64) > (1LL << 23)) return GSPN_ERR_SHAPE;
+    // 32-bit launches: at most one workgroup of 256 threads for 64 rows, or a
+    // request's rest, and 256 columns or 64 ranks
+    if ((a.T / 64 + a.N + 1) * std::max<int64_t>(4, (a.M + 255) / 256) > (1LL << 23)) return GSPN_ERR_SHAPE;
     return GSPN_OK;
 }
 

@@ -27,6 +27,7 @@
 // publishes its (A, B) before it waits for anything, whatever the offsets hold.
 #include "gspn_device.h"
 #include "gspn_kernels.h"
+#include "gspn_rows.h"
 
 namespace gspn {
 namespace {
@@ -68,52 +69,6 @@ constexpr float kKeepAll = -0.0f;                                               
 // at every token) would add up over the gate's memory, 1 / (1 - a) tokens;
 // that of 1 - a does not.
 __device__ __forceinline__ float keep(float s, float h) { return fmaf(s, h, open(s) ? h : 0.0f); }
-
-// ---------------------------------------------------------------- tiles
-struct Tile {
-    int64_t row;     // first row of the sequence
-    int64_t rows;    // rows of the sequence
-    int64_t n;       // the sequence (N: the rows behind the last)
-    int64_t j;       // which of its tiles; none of its rows are in it if j * kSeqTile >= rows
-};
-
-// Packed sequences take the tiles begin / kSeqTile + n and on: that gives each
-// at least ceil(rows / kSeqTile) tiles, and one, and needs no table.  Largest
-// n of 0 .. N whose first tile is not behind tile w; the lanes of a wave
-// compare 64 sequences at a time.  Whatever the offsets hold, the rows lie
-// inside the tensors.
-__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, int64_t T, int64_t N, uint32_t tiles,
-                                          uint32_t w, int lane) {
-    Tile r;
-    if (!offsets) {
-        r.n = w / tiles;   // tiles: of a sequence
-        r.j = w - (uint32_t)r.n * tiles;
-        r.rows = T / N;
-        r.row = r.n * r.rows;
-        return r;
-    }
-    auto clamped = [&](int64_t i) {
-        const int64_t o = offsets[i];
-        return o < 0 ? 0 : o > T ? T : o;
-    };
-    int64_t low = 0, count = N + 1;
-    while (count > 1) {
-        const int64_t step = (count + 63) / 64;
-        const int64_t i = lane * step;
-        const bool in_front = i < count && clamped(low + i) / kSeqTile + low + i <= w;
-        const uint64_t which = __ballot(in_front);
-        const int64_t skip = (which ? 63 - __clzll(which) : 0) * step;
-        low += skip;
-        count = count - skip < step ? count - skip : step;
-    }
-    const int64_t begin = clamped(low), end = low == N ? T : clamped(low + 1);
-    r.n = low;
-    r.row = begin;
-    r.rows = end > begin ? end - begin : 0;
-    r.j = (int64_t)w - begin / kSeqTile - low;
-    if (r.j < 0) r.j = r.rows / kSeqTile + 1;
-    return r;
-}
 
 // ---------------------------------------------------------------- tiles' results
 // What a tile tells the tiles behind it about one channel, in one 64-bit word
@@ -215,7 +170,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint32_t block = blockIdx.x % la.blocks;
     const uint32_t w = tile_number(la.counters, la.blocks, block, &number);
-    const Tile tile = find_tile(s.offsets, s.T, s.N, la.tiles, w, lane);
+    const Tile tile = find_tile<kSeqTile>(s.offsets, s.T, s.N, la.tiles, w, lane);
     const int64_t D = s.D;
     const int64_t d_own = (int64_t)block * (64 * V) + lane * V;
     const bool valid = d_own < D;
@@ -350,7 +305,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint32_t block = blockIdx.x % la.blocks;
     const uint32_t w = la.total - 1 - tile_number(la.counters, la.blocks, block, &number);
-    const Tile tile = find_tile(s.offsets, s.T, s.N, la.tiles, w, lane);
+    const Tile tile = find_tile<kSeqTile>(s.offsets, s.T, s.N, la.tiles, w, lane);
     const int64_t D = s.D;
     const int64_t d_own = (int64_t)block * (64 * V) + lane * V;
     const bool valid = d_own < D;
@@ -582,21 +537,12 @@ __global__ __launch_bounds__(256) void seq_step_kernel(gspn_seq_token s) {
 }
 
 // ---------------------------------------------------------------- host
-uint32_t tiles_of_sequence(const gspn_seq& s) {
-    const int64_t rows = s.T / s.N;
-    return (uint32_t)(rows > 0 ? (rows + kSeqTile - 1) / kSeqTile : 1);
-}
-
 // Whether a sequence may have two tiles.
 bool tiles_wait(const gspn_seq& s) { return (s.offsets ? s.T : s.T / s.N) > kSeqTile; }
 
-uint32_t total_tiles(const gspn_seq& s) {
-    return s.offsets ? (uint32_t)(s.T / kSeqTile + s.N + 1) : (uint32_t)s.N * tiles_of_sequence(s);
-}
-
 int64_t counter_bytes(const gspn_seq& s) { return (s.D + 63) / 64 * 64; }   // 64 for the narrowest block
 
-int64_t words_bytes(const gspn_seq& s) { return ((int64_t)total_tiles(s) * s.D * 8 + 15) / 16 * 16; }
+int64_t words_bytes(const gspn_seq& s) { return ((int64_t)total_tiles<kSeqTile>(s.offsets, s.T, s.N) * s.D * 8 + 15) / 16 * 16; }
 
 int power_of_two_in(int64_t v, int most) {
     int p = 1;
@@ -617,8 +563,8 @@ bool pairs(const gspn_seq& s) {
 Launch plan(const gspn_seq& s, int V) {
     Launch la;
     la.blocks = (uint32_t)((s.D + 64 * V - 1) / (64 * V));
-    la.tiles = s.offsets ? 0 : tiles_of_sequence(s);
-    la.total = total_tiles(s);
+    la.tiles = s.offsets ? 0 : tiles_of_sequence<kSeqTile>(s.T, s.N);
+    la.total = total_tiles<kSeqTile>(s.offsets, s.T, s.N);
     la.counters = nullptr;
     la.words = nullptr;
     if (tiles_wait(s)) {
