@@ -3,15 +3,20 @@
 //
 // Two launches over tiles of up to 64 rows of one request (gspn_rows.h):
 //  * shrink_kernel: v[t] = a[i] x[t], r numbers a row in fp32.  The long axis K
-//    is split over the four waves of a workgroup, which add up in LDS, and over
-//    `splits` workgroups, whose sums stay apart in the workspace.
-//  * expand_kernel: out[t] = base[t] + b[i] (scale[i] sum of the splits' v[t]);
-//    a wave owns the tile's rows of 64 columns at a time.
-// Both are matrix products on the matrix cores, with the adapter as the left
-// operand: lane l of a wave ends up with row l % 16 of the tile's, and
-// neighbouring ranks (columns) of it, so that v and out are written in whole
-// 16-byte pieces.  Tiles of up to 16 rows do a quarter of a full tile's
-// products: what a single token waits for is its adapter.
+//    is split over waves, which add up in LDS, and over `splits` workgroups,
+//    whose sums stay apart in the workspace.
+//  * expand_kernel: out[t] = base[t] + b[i] (scale[i] sum of the splits' v[t]),
+//    64 columns of 16 rows at a time.
+// Both are matrix products on the matrix cores.  An operand's lanes hold
+// different rows, so loading operands straight from memory asks for 64
+// addresses far apart with every instruction (measured: expand at 2.3 TB/s); so
+// every tile comes in whole row pieces, eight lanes to 128 bytes of a row, and
+// is turned in LDS, and the results go out the same way.  A wave turns its own
+// tiles in LDS of its own: no barriers, and what the next tile needs is loaded
+// while the present one is multiplied.
+//
+// Rows need not be aligned to 16 bytes: the pieces are read and written at
+// their elements' alignment, which the memory pipeline takes.
 #include "gspn_device.h"
 #include "gspn_kernels.h"
 #include "gspn_rows.h"
@@ -24,6 +29,7 @@ namespace {
 constexpr int kRows = 64;     // rows of a tile
 constexpr int kRB = kRows / 16;
 constexpr int kRanks = 64;    // ranks of a shrink workgroup
+constexpr int kWaves = 4;     // of a workgroup
 constexpr int kSplits = 16;   // workgroups that share K, at most
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -43,35 +49,84 @@ __device__ __forceinline__ void zero(Frag<float>& f) {
     for (int e = 0; e < 8; ++e) f.v[e] = 0.0f;
 }
 
-// p[0 .. 7], or those of them in front of `left` and zeros.  VEC: p is 16-byte
-// aligned and `left` a multiple of 8.
-template <bool VEC>
-__device__ __forceinline__ Frag<uint16_t> load8(const uint16_t* __restrict__ p, int64_t left) {
+// 16 and 8 bytes at the alignment of their elements.
+template <typename T> struct Piece;
+template <> struct Piece<uint16_t> {
+    typedef uint32_t x4 __attribute__((ext_vector_type(4), aligned(2)));
+    typedef uint32_t x2 __attribute__((ext_vector_type(2), aligned(2)));
+};
+template <> struct Piece<float> { typedef float x4 __attribute__((ext_vector_type(4), aligned(4))); };
+
+__device__ __forceinline__ Frag<uint16_t> load8(const uint16_t* __restrict__ p) {
     Frag<uint16_t> f;
-    if constexpr (VEC) {
-        if (left > 0) f.v = *reinterpret_cast<const bf16x8*>(p);
-        else zero(f);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f.v[e] = __builtin_bit_cast(__bf16, e < left ? p[e] : (uint16_t)0);
-    }
+    f.v = __builtin_bit_cast(bf16x8, (u32x4)*reinterpret_cast<const Piece<uint16_t>::x4*>(p));
     return f;
 }
-template <bool VEC>
-__device__ __forceinline__ Frag<float> load8(const float* __restrict__ p, int64_t left) {
+__device__ __forceinline__ Frag<float> load8(const float* __restrict__ p) {
     Frag<float> f;
-    if constexpr (VEC) {
-        if (left > 0) {
-            const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
+    const f32x4 lo = *reinterpret_cast<const Piece<float>::x4*>(p), hi = *reinterpret_cast<const Piece<float>::x4*>(p + 4);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f.v[e] = lo[e], f.v[4 + e] = hi[e];
-        } else {
-            zero(f);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f.v[e] = e < left ? p[e] : 0.0f;
+    for (int e = 0; e < 4; ++e) f.v[e] = lo[e], f.v[4 + e] = hi[e];
+    return f;
+}
+// Those of p[0 .. 7] in front of `left`, and zeros.
+__device__ __forceinline__ Frag<uint16_t> load8(const uint16_t* __restrict__ p, int64_t left) {
+    if (left >= 8) return load8(p);
+    Frag<uint16_t> f;
+    zero(f);
+    if (left <= 0) return f;
+    if (left == 4) {
+        const auto v = *reinterpret_cast<const Piece<uint16_t>::x2*>(p);
+        f.v = __builtin_bit_cast(bf16x8, u32x4{v.x, v.y, 0, 0});
+        return f;
     }
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < left) f.v[e] = __builtin_bit_cast(__bf16, p[e]);
+    return f;
+}
+__device__ __forceinline__ Frag<float> load8(const float* __restrict__ p, int64_t left) {
+    if (left >= 8) return load8(p);
+    Frag<float> f;
+    zero(f);
+    if (left >= 4) {
+        const f32x4 v = *reinterpret_cast<const Piece<float>::x4*>(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f.v[e] = v[e];
+#pragma unroll
+        for (int e = 4; e < 7; ++e)
+            if (e < left) f.v[e] = p[e];
+        return f;
+    }
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+        if (e < left) f.v[e] = p[e];
+    return f;
+}
+
+// Lanes of a wave hand each other data through LDS.  A wave's accesses to LDS
+// complete in their order; this keeps the compiler to that order.
+__device__ __forceinline__ void handover() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Eight elements to and from LDS (16-byte aligned there).
+__device__ __forceinline__ void keep8(uint16_t* p, const Frag<uint16_t>& f) { *reinterpret_cast<bf16x8*>(p) = f.v; }
+__device__ __forceinline__ void keep8(float* p, const Frag<float>& f) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{f.v[0], f.v[1], f.v[2], f.v[3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{f.v[4], f.v[5], f.v[6], f.v[7]};
+}
+__device__ __forceinline__ Frag<uint16_t> kept8(const uint16_t* p) {
+    Frag<uint16_t> f;
+    f.v = *reinterpret_cast<const bf16x8*>(p);
+    return f;
+}
+__device__ __forceinline__ Frag<float> kept8(const float* p) {
+    Frag<float> f;
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f.v[e] = lo[e], f.v[4 + e] = hi[e];
     return f;
 }
 
@@ -117,14 +172,20 @@ struct Launch {
     int64_t slice;      // shrink: K of a workgroup, a multiple of 64
     int64_t pitch;      // ranks of a row of v: r rounded up to 16
     uint32_t parts;     // expand: workgroups that share M
-    int64_t columns;    // expand: columns of a wave, a multiple of 64
+    int64_t columns;    // expand: columns of a workgroup, a multiple of 256
 };
 
 // ---------------------------------------------------------------- shrink
 // RB: blocks of 16 ranks of the workgroup.
-template <typename T, int RB, bool VEC>
-__global__ __launch_bounds__(256) void shrink_kernel(gspn_adapter s, Launch la) {
-    __shared__ f32x4 sums[4][kRB * RB][64];
+template <typename T, int RB>
+__global__ __launch_bounds__(kWaves * 64, 2) void shrink_kernel(gspn_adapter s, Launch la) {
+    constexpr int kWide = 128 / sizeof(T);          // elements of K of a wave's tile: 128 bytes of a row
+    constexpr int kPitch = kWide + 16 / sizeof(T);  // in LDS; 16 bytes more spread the rows over the banks
+    constexpr int kPieces = kWide / 8;              // pieces of eight elements of a row
+    constexpr int kAtOnce = 64 / kPieces;           // rows of a wave's load
+    constexpr int kStage = (kRB + RB) * 16 * kPitch * sizeof(T);   // bytes of LDS of a wave
+    __shared__ __attribute__((aligned(16))) char lds[kWaves * kStage];
+    static_assert(kStage >= kRB * RB * 64 * 16, "the sums take the tiles' place");
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int q = lane >> 4, c = lane & 15;
     const uint32_t split = blockIdx.x % la.splits, rest = blockIdx.x / la.splits;
@@ -136,57 +197,84 @@ __global__ __launch_bounds__(256) void shrink_kernel(gspn_adapter s, Launch la) 
     if (id < 0 || id >= s.R) return;
     const int count = uniform((int)(tile.rows - start < kRows ? tile.rows - start : kRows));
     const int64_t row = tile.row + start;
-
-    const T* __restrict__ ap[RB];
-    const T* __restrict__ xp[kRB];
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        // ranks behind the last read it again; their sums are not kept
-        const int64_t j = (int64_t)group * kRanks + i * 16 + c;
-        ap[i] = static_cast<const T*>(s.a) + (id * s.r + (j < s.r ? j : s.r - 1)) * s.K + 8 * q;
-    }
-#pragma unroll
-    for (int i = 0; i < kRB; ++i) {
-        const int t = i * 16 + c;   // rows behind the last likewise
-        xp[i] = static_cast<const T*>(s.x) + (row + (t < count ? t : count - 1)) * s.x_stride + 8 * q;
-    }
     const int64_t end = ((int64_t)split + 1) * la.slice < s.K ? ((int64_t)split + 1) * la.slice : s.K;
+    f32x4* sums = reinterpret_cast<f32x4*>(lds);    // [kWaves][kRB * RB][64]
+
     auto products = [&](auto blocks) {
-        constexpr int NB = decltype(blocks)::value;   // blocks of 16 rows
-        f32x4 acc[NB][RB] = {};
-        for (int64_t k = (int64_t)split * la.slice + wave * 64; k < end; k += 256) {
-            Frag<T> a[2][RB], x[2][NB];
+        constexpr int NB = decltype(blocks)::value;                       // blocks of 16 rows
+        constexpr int NX = NB * 16 / kAtOnce, NA = RB * 16 / kAtOnce;     // loads of a tile
+        T* xs = reinterpret_cast<T*>(lds + wave * kStage);
+        T* as = xs + NB * 16 * kPitch;
+        const int piece = lane % kPieces, line = lane / kPieces;
+        const T* __restrict__ xp[NX];
+        const T* __restrict__ ap[NA];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t at = k + 32 * h, left = s.K - at - 8 * q;
-#pragma unroll
-                for (int i = 0; i < RB; ++i) a[h][i] = load8<VEC>(ap[i] + at, left);
-#pragma unroll
-                for (int t = 0; t < NB; ++t) x[h][t] = load8<VEC>(xp[t] + at, left);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int t = 0; t < NB; ++t)
-#pragma unroll
-                    for (int i = 0; i < RB; ++i) multiply(acc[t][i], a[h][i], x[h][t]);
+        for (int i = 0; i < NX; ++i) {
+            const int t = i * kAtOnce + line;   // rows behind the last read it again
+            xp[i] = static_cast<const T*>(s.x) + (row + (t < count ? t : count - 1)) * s.x_stride + 8 * piece;
         }
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            // ranks behind the last likewise; their sums are not kept
+            const int64_t j = (int64_t)group * kRanks + i * kAtOnce + line;
+            ap[i] = static_cast<const T*>(s.a) + (id * s.r + (j < s.r ? j : s.r - 1)) * s.K + 8 * piece;
+        }
+        Frag<T> x[NX], a[NA];
+        auto load = [&](int64_t k) {
+            if (k + kWide <= end) {
+#pragma unroll
+                for (int i = 0; i < NX; ++i) x[i] = load8(xp[i] + k);
+#pragma unroll
+                for (int i = 0; i < NA; ++i) a[i] = load8(ap[i] + k);
+            } else {
+                const int64_t left = end - k - 8 * piece;
+#pragma unroll
+                for (int i = 0; i < NX; ++i) x[i] = load8(xp[i] + k, left);
+#pragma unroll
+                for (int i = 0; i < NA; ++i) a[i] = load8(ap[i] + k, left);
+            }
+        };
+        f32x4 acc[NB][RB] = {};
+        int64_t k = (int64_t)split * la.slice + wave * kWide;
+        if (k < end) load(k);
+        for (; k < end; k += kWaves * kWide) {
+#pragma unroll
+            for (int i = 0; i < NX; ++i) keep8(xs + (i * kAtOnce + line) * kPitch + 8 * piece, x[i]);
+#pragma unroll
+            for (int i = 0; i < NA; ++i) keep8(as + (i * kAtOnce + line) * kPitch + 8 * piece, a[i]);
+            handover();
+            if (k + kWaves * kWide < end) load(k + kWaves * kWide);
+#pragma unroll
+            for (int h = 0; h < kWide / 32; ++h) {
+                Frag<T> fa[RB];
+#pragma unroll
+                for (int i = 0; i < RB; ++i) fa[i] = kept8(as + (i * 16 + c) * kPitch + 32 * h + 8 * q);
+#pragma unroll
+                for (int t = 0; t < NB; ++t) {
+                    const Frag<T> fx = kept8(xs + (t * 16 + c) * kPitch + 32 * h + 8 * q);
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) multiply(acc[t][i], fa[i], fx);
+                }
+            }
+            handover();
+        }
+        __syncthreads();   // every wave is done with its tiles
 #pragma unroll
         for (int t = 0; t < NB; ++t)
 #pragma unroll
-            for (int i = 0; i < RB; ++i) sums[wave][t * RB + i][lane] = acc[t][i];
+            for (int i = 0; i < RB; ++i) sums[(wave * kRB * RB + t * RB + i) * 64 + lane] = acc[t][i];
     };
     // one block of rows, or all four (rows behind the last are copies of it)
     if (count <= 16) products(std::integral_constant<int, 1>());
     else products(std::integral_constant<int, kRB>());
     __syncthreads();
     float* __restrict__ v = static_cast<float*>(s.work) + (size_t)split * s.T * la.pitch;
-    for (int b = wave; b < kRB * RB; b += 4) {
+    for (int b = wave; b < kRB * RB; b += kWaves) {
         const int t = (b / RB) * 16 + c, i = b % RB;
         if (t >= count) continue;
-        f32x4 sum = sums[0][b][lane];
+        f32x4 sum = sums[b * 64 + lane];
 #pragma unroll
-        for (int o = 1; o < 4; ++o) sum += sums[o][b][lane];
+        for (int o = 1; o < kWaves; ++o) sum += sums[(o * kRB * RB + b) * 64 + lane];
         const int64_t j = (int64_t)group * kRanks + i * 16 + 4 * q;
         if (j >= la.pitch) continue;
 #pragma unroll
@@ -197,39 +285,21 @@ __global__ __launch_bounds__(256) void shrink_kernel(gspn_adapter s, Launch la) 
 }
 
 // ---------------------------------------------------------------- expand
-// Sixteen neighbouring columns of a row: out = base + sum, or base, or 0.
-template <typename T, bool VEC>
-__device__ __forceinline__ void finish(const T* base, T* out, int64_t left, const f32x4 (&sum)[4]) {
-    if constexpr (VEC && sizeof(T) == 2) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (8 * h >= left) break;
-            const u32x4 b = *reinterpret_cast<const u32x4*>(base + 8 * h);
-            u32x4 o;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const f32x4& f = sum[2 * h + e / 2];
-                o[e] = pack_bf16x2(bf16_lo(b[e]) + f[2 * (e & 1)], bf16_hi(b[e]) + f[2 * (e & 1) + 1]);
-            }
-            *reinterpret_cast<u32x4*>(out + 8 * h) = o;
-        }
-    } else if constexpr (VEC) {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            if (4 * h >= left) break;
-            *reinterpret_cast<f32x4*>(out + 4 * h) = *reinterpret_cast<const f32x4*>(base + 4 * h) + sum[h];
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (e < left) out[e] = from_f32(to_f32(base[e]) + sum[e / 4][e % 4], (T*)nullptr);
-    }
-}
-
 // STEPS: steps of 32 ranks whose v a wave keeps for all its columns; 0: any
-// number, v is read again for every 64 columns.
-template <typename T, int STEPS, bool VEC>
-__global__ __launch_bounds__(256) void expand_kernel(gspn_adapter s, Launch la) {
+// number, one or two steps at a time, v is read again for every 64 columns.
+// EIGHTS: r is a multiple of 8.
+template <typename T, int STEPS, bool EIGHTS>
+__global__ __launch_bounds__(kWaves * 64, 2) void expand_kernel(gspn_adapter s, Launch la) {
+    constexpr int kSteps = STEPS ? STEPS : sizeof(T) == 2 ? 2 : 1;
+    constexpr int kPitch = 32 * kSteps + 16 / sizeof(T);   // of b's rows in LDS
+    constexpr int kOPitch = 64 + 4;                        // of a row of sums, fp32
+    constexpr int kStage = 64 * kPitch * sizeof(T);        // bytes of LDS of a wave; the sums take b's place
+    static_assert(kStage >= 16 * kOPitch * 4, "the sums take b's place");
+    constexpr int kLoads = 4 * kSteps;                     // pieces of eight elements of b for a lane
+    constexpr int kOut = 16 * 64 * sizeof(T) / 1024;       // 16-byte pieces of base for a lane
+    constexpr int kPer = 16 / sizeof(T);                   // elements of such a piece
+    __shared__ __attribute__((aligned(16))) char lds[kWaves * kStage];
+    typedef typename Piece<T>::x4 Out;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int q = lane >> 4, c = lane & 15;
     const uint32_t part = blockIdx.x % la.parts, w = blockIdx.x / la.parts;
@@ -237,90 +307,174 @@ __global__ __launch_bounds__(256) void expand_kernel(gspn_adapter s, Launch la) 
     const int64_t start = tile.j * kRows;
     if (start >= tile.rows) return;
     const int count = uniform((int)(tile.rows - start < kRows ? tile.rows - start : kRows));
-    const int64_t row = tile.row + start;
-    const int64_t first = ((int64_t)part * 4 + wave) * la.columns;
-    const int64_t last = first + la.columns < s.M ? first + la.columns : s.M;
     const T* base = static_cast<const T*>(s.base);   // may be out itself: a lane reads what it then writes
     T* out = static_cast<T*>(s.out);
+    // the waves of up to 16 rows share the columns, those of more have 16 rows each
+    int64_t first = part * la.columns;
+    const int64_t last = first + la.columns < s.M ? first + la.columns : s.M;
+    int block = wave, stride = 64;
+    if (count <= 16) block = 0, first += 64 * wave, stride = 64 * kWaves;
+    const int mine = count - block * 16 < 16 ? count - block * 16 : 16;   // rows of this wave
+    if (mine <= 0 || first >= last) return;
+    const int64_t row = tile.row + start + block * 16;
     const int64_t id = tile.n == s.N ? -1 : s.ids[tile.n];
     if (tile.n == s.N || id < 0 || id >= s.R) {
         // rows of no request (zero, or as they were), or of one without an adapter (base's)
         if (tile.n == s.N ? !(s.flags & GSPN_SEQ_ZERO_TAIL) : base == out) return;
-        for (int t = 0; t < count; ++t)
-            for (int64_t m = first + lane; m < last; m += 64)
+        for (int t = 0; t < mine; ++t)
+            for (int64_t m = first + lane; m < last; m += stride)
                 out[(row + t) * s.out_stride + m] =
                     tile.n == s.N ? from_f32(0.0f, (T*)nullptr) : base[(row + t) * s.base_stride + m];
         return;
     }
+    T* bs = reinterpret_cast<T*>(lds + wave * kStage);
+    float* os = reinterpret_cast<float*>(lds + wave * kStage);
     const float scale = s.scale ? s.scale[id] : 1.0f;
-    // v of row 16 t + c, ranks 32 k + 8 q .. + 7: the splits' sums, scaled
-    auto load_v = [&](int t, int k) {
-        const int at = t * 16 + c;
-        const int64_t j = 32 * k + 8 * q;
-        const float* __restrict__ p =
-            static_cast<const float*>(s.work) + (size_t)(row + (at < count ? at : count - 1)) * la.pitch + j;
+    // v of the lane's row, ranks 32 k + 8 q .. + 7: the splits' sums, scaled
+    // (rows behind the last read it again)
+    const float* __restrict__ vp =
+        static_cast<const float*>(s.work) + (size_t)(row + (c < mine ? c : mine - 1)) * la.pitch + 8 * q;
+    auto load_v = [&](int k) {
         f32x4 lo = {}, hi = {};
-        if (j < la.pitch)
+        if (32 * k + 8 * q < la.pitch) {
+            const float* __restrict__ p = vp + 32 * k;
             for (uint32_t i = 0; i < la.splits; ++i, p += s.T * la.pitch) {
                 lo += *reinterpret_cast<const f32x4*>(p);
                 hi += *reinterpret_cast<const f32x4*>(p + 4);
             }
+        }
         Parts<T> f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) f.set(e, scale * lo[e]), f.set(4 + e, scale * hi[e]);
         return f;
     };
-    constexpr int kKeep = STEPS ? STEPS : 1;
+    Parts<T> v[kSteps];
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) v[k] = load_v(k);
+
+    // b of 64 columns and up to 32 kSteps ranks from rank j0 on: rows of LDS,
+    // zeros behind the last rank
     const T* __restrict__ bp = static_cast<const T*>(s.b) + id * s.M * s.r;
-    auto columns = [&](auto blocks) {
-        constexpr int NB = decltype(blocks)::value;   // blocks of 16 rows
-        Parts<T> v[NB][kKeep];
-        if constexpr (STEPS != 0) {
+    Frag<T> b[kLoads];
+    auto load_b = [&](int64_t m, int64_t j0) {
+        const int64_t ranks = s.r - j0 < 32 * kSteps ? s.r - j0 : 32 * kSteps;
+        const int pieces = (int)(ranks / 8);
 #pragma unroll
-            for (int t = 0; t < NB; ++t)
-#pragma unroll
-                for (int k = 0; k < STEPS; ++k) v[t][k] = load_v(t, k);
-        }
-        for (int64_t m = first; m < last; m += 64) {
-            f32x4 acc[NB][4] = {};
-            // block i of 16 columns holds m + 16 (row / 4) + 4 i + row % 4: lane l's
-            // sums of the four blocks are sixteen neighbouring columns, m + 16 q on
-            int64_t column[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t o = m + 16 * (c >> 2) + 4 * i + (c & 3);
-                column[i] = o < s.M ? o : s.M - 1;   // columns behind the last read it again
-            }
-            auto step = [&](int k, int slot) {
-                const int64_t j = 32 * k + 8 * q;
-                Frag<T> b[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) b[i] = load8<VEC>(bp + column[i] * s.r + j, s.r - j);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int t = 0; t < NB; ++t) multiply(acc[t][i], b[i], v[t][slot]);
-            };
-            if constexpr (STEPS != 0) {
-#pragma unroll
-                for (int k = 0; k < STEPS; ++k) step(k, k);
-            } else {
-                for (int k = 0; 32 * k < s.r; ++k) {
-#pragma unroll
-                    for (int t = 0; t < NB; ++t) v[t][0] = load_v(t, k);
-                    step(k, 0);
-                }
-            }
-            const int64_t at = m + 16 * q, left = s.M - at;
-#pragma unroll
-            for (int t = 0; t < NB; ++t)
-                if (t * 16 + c < count && left > 0)
-                    finish<T, VEC>(base + (row + t * 16 + c) * s.base_stride + at,
-                                   out + (row + t * 16 + c) * s.out_stride + at, left, acc[t]);
+        for (int i = 0; i < kLoads; ++i) {
+            if (i >= pieces) break;
+            const int e = i * 64 + lane;
+            const int64_t o = m + e / pieces;   // columns behind the last read it again
+            b[i] = load8(bp + (o < s.M ? o : s.M - 1) * s.r + j0 + 8 * (e % pieces));
         }
     };
-    if (count <= 16) columns(std::integral_constant<int, 1>());
-    else columns(std::integral_constant<int, kRB>());
+    auto keep_b = [&](int64_t m, int64_t j0) {
+        const int64_t ranks = s.r - j0 < 32 * kSteps ? s.r - j0 : 32 * kSteps;
+        if constexpr (EIGHTS) {
+            const int pieces = (int)(ranks / 8);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                if (i >= pieces) break;
+                const int e = i * 64 + lane;
+                keep8(bs + (e / pieces) * kPitch + 8 * (e % pieces), b[i]);
+            }
+            // a step's empty pieces (the sums before this tile lay here)
+            for (int p = pieces + q; p < (pieces + 3) / 4 * 4; p += 4) {
+                Frag<T> none;
+                zero(none);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) keep8(bs + (16 * i + c) * kPitch + 8 * p, none);
+            }
+        } else {
+            // one column a lane; columns behind the last read it again
+            const int64_t o = m + lane < s.M ? m + lane : s.M - 1;
+            const T* __restrict__ p = bp + o * s.r + j0;
+            for (int64_t j = 0; j < (ranks + 31) / 32 * 32; j += 8) keep8(bs + lane * kPitch + j, load8(p + j, ranks - j));
+        }
+    };
+    // base of 16 rows of 64 columns, in pieces of whole rows
+    constexpr int kLine = 64 / kPer;   // lanes of a row
+    const int oc = (lane % kLine) * kPer, orow = lane / kLine;
+    Out old[kOut];
+    auto load_base = [&](int64_t m) {
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) {
+            const int t = i * (64 / kLine) + orow;
+            if (t < mine && m + oc + kPer <= s.M)
+                old[i] = *reinterpret_cast<const Out*>(base + (row + t) * s.base_stride + m + oc);
+        }
+    };
+    if constexpr (EIGHTS) load_b(first, 0);
+    load_base(first);
+    for (int64_t m = first; m < last; m += stride) {
+        f32x4 acc[4] = {};
+        Out now[kOut];
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) now[i] = old[i];
+        const bool more = m + stride < last;
+        for (int64_t j0 = 0; j0 < (STEPS ? 1 : s.r); j0 += 32 * kSteps) {
+            keep_b(m, j0);
+            handover();
+            if constexpr (STEPS == 0) {
+                const int64_t next = j0 + 32 * kSteps;
+                if constexpr (EIGHTS) {
+                    if (next < s.r) load_b(m, next);
+                    else if (more) load_b(m + stride, 0);
+                }
+                if (j0 == 0 && more) load_base(m + stride);
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) v[k] = load_v((int)(j0 / 32) + k);
+            } else if (more) {
+                if constexpr (EIGHTS) load_b(m + stride, 0);
+                load_base(m + stride);
+            }
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                if (j0 + 32 * k >= s.r) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    multiply(acc[i], kept8(bs + (16 * i + c) * kPitch + 32 * k + 8 * q), v[k]);
+            }
+            handover();
+        }
+        // lane l holds row c of the columns 16 i + 4 q .. + 3
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(os + c * kOPitch + 16 * i + 4 * q) = acc[i];
+        handover();
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) {
+            const int t = i * (64 / kLine) + orow;
+            float sum[kPer];
+#pragma unroll
+            for (int e = 0; e < kPer; e += 4) {
+                const f32x4 f = *reinterpret_cast<const f32x4*>(os + t * kOPitch + oc + e);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sum[e + k] = f[k];
+            }
+            if (t >= mine) continue;
+            const int64_t left = s.M - m - oc;
+            T* po = out + (row + t) * s.out_stride + m + oc;
+            if (left >= kPer) {
+                if constexpr (sizeof(T) == 2) {
+                    Out o;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[e] = pack_bf16x2(bf16_lo(now[i][e]) + sum[2 * e], bf16_hi(now[i][e]) + sum[2 * e + 1]);
+                    *reinterpret_cast<Out*>(po) = o;
+                } else {
+                    Out o;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = now[i][e] + sum[e];
+                    *reinterpret_cast<Out*>(po) = o;
+                }
+            } else {
+                const T* pb = base + (row + t) * s.base_stride + m + oc;
+#pragma unroll
+                for (int e = 0; e < kPer - 1; ++e)
+                    if (e < left) po[e] = from_f32(to_f32(pb[e]) + sum[e], (T*)nullptr);
+            }
+        }
+        handover();
+    }
 }
 
 // ---------------------------------------------------------------- host
@@ -331,37 +485,32 @@ Launch plan(const gspn_adapter& s) {
     la.total = total_tiles<kRows>(s.offsets, s.T, s.N);
     la.groups = (uint32_t)((s.r + kRanks - 1) / kRanks);
     la.pitch = (s.r + 15) / 16 * 16;
-    // K is shared by more workgroups while there are fewer than some four for
-    // a CU, as long as each of their waves has 64 of it
-    const int64_t blocks = (s.K + 63) / 64, most = std::min<int64_t>(kSplits, (blocks + 3) / 4);
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most, 1024 / ((int64_t)la.total * la.groups)));
+    // K is shared by more workgroups while there are fewer than two for a CU,
+    // as long as each of their waves has 64 of it
+    const int64_t blocks = (s.K + 63) / 64, most = std::min<int64_t>(kSplits, (blocks + kWaves - 1) / kWaves);
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most, 512 / ((int64_t)la.total * la.groups)));
     la.slice = (blocks + want - 1) / want * 64;
     la.splits = (uint32_t)((s.K + la.slice - 1) / la.slice);
-    // a wave takes up to four times 64 columns while workgroups are many
-    int64_t columns = 64;
-    while (columns < 256 && la.total * ((s.M + 4 * columns - 1) / (4 * columns)) > 2048) columns *= 2;
+    // a workgroup takes up to 1024 columns while workgroups are many
+    int64_t columns = 256;
+    while (columns < 1024 && la.total * ((s.M + columns - 1) / columns) > 2048) columns *= 2;
     la.columns = columns;
-    la.parts = (uint32_t)((s.M + 4 * columns - 1) / (4 * columns));
+    la.parts = (uint32_t)((s.M + columns - 1) / columns);
     return la;
 }
 
-bool aligned(const void* p, int64_t stride, int64_t to) { return ((uintptr_t)p & 15) == 0 && stride % to == 0; }
-
 template <typename T>
 void launch_typed(const gspn_adapter& s, const Launch& la, hipStream_t stream) {
-    constexpr int64_t to = 16 / sizeof(T);   // elements of a 16-byte piece
-    const dim3 gs(la.total * la.groups * la.splits), ge(la.total * la.parts), threads(256);
-    const bool vs = s.K % 8 == 0 && aligned(s.a, 0, to) && aligned(s.x, s.x_stride, to);
-    const bool ve = s.r % 8 == 0 && s.M % 8 == 0 && aligned(s.b, 0, to) && aligned(s.base, s.base_stride, to) &&
-                    aligned(s.out, s.out_stride, to);
-    auto shrink = [&](auto kernel) { hipLaunchKernelGGL(kernel, gs, threads, 0, stream, s, la); };
-    auto expand = [&](auto kernel) { hipLaunchKernelGGL(kernel, ge, threads, 0, stream, s, la); };
-    if (s.r <= 16) vs ? shrink(shrink_kernel<T, 1, true>) : shrink(shrink_kernel<T, 1, false>);
-    else if (s.r <= 32) vs ? shrink(shrink_kernel<T, 2, true>) : shrink(shrink_kernel<T, 2, false>);
-    else vs ? shrink(shrink_kernel<T, 4, true>) : shrink(shrink_kernel<T, 4, false>);
-    if (s.r <= 32) ve ? expand(expand_kernel<T, 1, true>) : expand(expand_kernel<T, 1, false>);
-    else if (s.r <= 64) ve ? expand(expand_kernel<T, 2, true>) : expand(expand_kernel<T, 2, false>);
-    else ve ? expand(expand_kernel<T, 0, true>) : expand(expand_kernel<T, 0, false>);
+    const dim3 gs(la.total * la.groups * la.splits), ge(la.total * la.parts);
+    auto shrink = [&](auto kernel) { hipLaunchKernelGGL(kernel, gs, dim3(kWaves * 64), 0, stream, s, la); };
+    auto expand = [&](auto kernel) { hipLaunchKernelGGL(kernel, ge, dim3(kWaves * 64), 0, stream, s, la); };
+    if (s.r <= 16) shrink(shrink_kernel<T, 1>);
+    else if (s.r <= 32) shrink(shrink_kernel<T, 2>);
+    else shrink(shrink_kernel<T, 4>);
+    const bool eights = s.r % 8 == 0;
+    if (s.r <= 32) eights ? expand(expand_kernel<T, 1, true>) : expand(expand_kernel<T, 1, false>);
+    else if (s.r <= 64) eights ? expand(expand_kernel<T, 2, true>) : expand(expand_kernel<T, 2, false>);
+    else eights ? expand(expand_kernel<T, 0, true>) : expand(expand_kernel<T, 0, false>);
 }
 
 }  // namespace

@@ -757,9 +757,9 @@ int check_adapter_sizes(const gspn_adapter& a) {
         return GSPN_ERR_SHAPE;
     if (!a.offsets && a.T % a.N) return GSPN_ERR_SHAPE;
     if (check_dtype(a.dtype)) return GSPN_ERR_DTYPE;
-    // 32-bit launches: at most one workgroup of 256 threads for 64 rows, or a
+    // 32-bit launches: at most one workgroup of 512 threads for 64 rows, or a
     // request's rest, and 256 columns or 64 ranks
-    if ((a.T / 64 + a.N + 1) * std::max<int64_t>(4, (a.M + 255) / 256) > (1LL << 23)) return GSPN_ERR_SHAPE;
+    if ((a.T / 64 + a.N + 1) * std::max<int64_t>(4, (a.M + 255) / 256) > (1LL << 22)) return GSPN_ERR_SHAPE;
     return GSPN_OK;
 }
 

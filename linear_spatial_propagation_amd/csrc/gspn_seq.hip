@@ -15,16 +15,18 @@
 //    every input is read once;
 //  * each wave forms its stretch's (A, B), the waves join theirs in LDS, and
 //    the workgroup publishes the tile's;
-//  * a tile that is not its sequence's first adds up what the tiles in front
-//    of it published until it meets one whose own state in front is known
-//    (look_back), and publishes the state behind itself;
+//  * a tile that is not its sequence's first looks back over the tiles in front
+//    of it to one that has published the state behind itself, goes from there
+//    through the (A, B) of those between, and publishes its own state;
 //  * with the state in front of its tokens, each wave finishes them.
 // A tile never holds rows of two sequences, so nothing passes between them.
 //
 // Every wait ends: workgroups take their tile from a counter (one for each
-// block of channels), wait only for tiles of the same block with smaller
-// numbers, and so only for workgroups that already run; and each of those
-// publishes its (A, B) before it waits for anything, whatever the offsets hold.
+// block of channels) and wait only for tiles of the same block with smaller
+// numbers, and so only for workgroups that already run.  Each of those publishes
+// its (A, B) before it waits, and its state when its own wait ends; the one with
+// the smallest number, and whatever tile the offsets make the first of a
+// sequence, waits for nobody.
 #include "gspn_device.h"
 #include "gspn_kernels.h"
 #include "gspn_rows.h"
@@ -89,17 +91,23 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* p) {
 
 // The state that the `most` >= 1 tiles before this one (the words of tile i are
 // `stride` further each, i = 1 the nearest; the furthest is the sequence's
-// end) leave in front of it.  Every wave looks at one tile a round and the
-// waves join theirs through `board`.
+// end) leave in front of it.  Every wave looks at one tile a round, kWaves tiles
+// further each round, until for each channel one of them has said its state;
+// from there the (A, B) of the nearer ones lead back, h -> A h + B one tile after
+// the other.  That is the arithmetic by which those tiles get their own states, so
+// the result does not depend on who was first.  Behind kWindow tiles without a
+// state the furthest are asked again: the first tile of a sequence waits for
+// nobody, so each one after it gets its state in turn.
+constexpr int kWindow = 32;
+
 template <int V>
 __device__ __forceinline__ void look_back(const uint64_t* words, int64_t stride, int64_t most, int wave, int lane,
-                                          float2 (&board)[kWaves][V][64], float (&carry)[V]) {
-    float A[V], B[V];
-    bool done[V];
+                                          float2 (&board)[kWindow][V][64], float (&carry)[V]) {
+    int from[V];   // the nearest tile that said its state, 0: none yet
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f, done[v] = false;
-    for (int64_t first = 1;; first += kWaves) {
-        const int64_t i = first + wave;
+    for (int v = 0; v < V; ++v) from[v] = 0;
+    for (int first = 0;; first = first + kWaves < kWindow ? first + kWaves : first) {
+        const int64_t i = first + wave + 1;
         if (i <= most) {
             const uint64_t* p = words + i * stride;
             uint64_t word[V];
@@ -117,30 +125,31 @@ __device__ __forceinline__ void look_back(const uint64_t* words, int64_t stride,
             for (int v = 0; v < V; ++v) {
                 // a sequence's furthest tile says its state; anything else there is an end too
                 const bool state = (uint32_t)(word[v] >> 32) == kState || i == most;
-                board[wave][v][lane] = make_float2(state ? -1.0f : __uint_as_float((uint32_t)(word[v] >> 32)),
-                                                   __uint_as_float((uint32_t)word[v]));
+                board[first + wave][v][lane] = make_float2(state ? -1.0f : __uint_as_float((uint32_t)(word[v] >> 32)),
+                                                           __uint_as_float((uint32_t)word[v]));
             }
         }
         __syncthreads();
         bool every = true;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            for (int k = 0; k < kWaves && first + k <= most; ++k) {
-                const float2 f = board[k][v][lane];
-                if (!done[v]) {
-                    B[v] = fmaf(A[v], f.y, B[v]);
-                    if (f.x == -1.0f) done[v] = true;
-                    else A[v] *= f.x;
-                }
-            }
-            every = every && done[v];
+            for (int k = first; k < first + kWaves && k < most; ++k)
+                if (!from[v] && board[k][v][lane].x == -1.0f) from[v] = k + 1;
+            every = every && from[v];
         }
         // the same in every wave: all of them read the same board
         if (__all(every)) break;
         __syncthreads();
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = B[v];
+    for (int v = 0; v < V; ++v) {
+        float h = board[from[v] - 1][v][lane].y;
+        for (int k = from[v] - 2; k >= 0; --k) {
+            const float2 f = board[k][v][lane];
+            h = fmaf(f.x, h, f.y);
+        }
+        carry[v] = h;
+    }
 }
 
 // The workgroup's tile: from the counter where tiles wait for each other.
@@ -165,7 +174,7 @@ template <typename T, int V, bool SHARED, bool LAM, bool U>
 __global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch la) {
     using R = typename Raw<T, V>::type;
     using RG = typename Raw<T, SHARED ? 1 : V>::type;
-    __shared__ float2 parts[kWaves][V][64], board[kWaves][V][64];
+    __shared__ float2 parts[kWaves][V][64], board[kWindow][V][64];
     __shared__ uint32_t number;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint32_t block = blockIdx.x % la.blocks;
@@ -299,7 +308,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
                                                               float* __restrict__ partial) {
     using R = typename Raw<T, V>::type;
     using RG = typename Raw<T, SHARED ? 1 : V>::type;
-    __shared__ float2 parts[kWaves][V][64], board[kWaves][V][64];
+    __shared__ float2 parts[kWaves][V][64], board[kWindow][V][64];
     __shared__ float back[kWaves][V][64];
     __shared__ uint32_t number;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
