@@ -54,23 +54,50 @@ __device__ __forceinline__ void put(uint16_t* p, const float (&v)[2]) {
 }
 __device__ __forceinline__ void put(float* p, const float (&v)[1]) { *p = v[0]; }
 
+// A walk down the rows of a tensor: the row is the same for a wave's lanes (a
+// scalar register), a lane's place in it a 32-bit offset.
+template <typename T> struct Walk {
+    const char* p;
+    int64_t step;
+    __device__ Walk(const void* base, int64_t row, int64_t stride)
+        : p(static_cast<const char*>(base) + row * stride * (int64_t)sizeof(T)), step(stride * (int64_t)sizeof(T)) {}
+    template <typename R> __device__ R at(uint32_t offset) const { return *reinterpret_cast<const R*>(p + offset); }
+    __device__ T* out(uint32_t offset) const { return reinterpret_cast<T*>(const_cast<char*>(p) + offset); }
+    __device__ void down(bool go = true) { p += go ? step : 0; }
+    __device__ void up() { p -= step; }
+};
+
 // ---------------------------------------------------------------- gates
-// A gate is held as one number that loses no precision for a near 0 or near 1:
-// the smaller of a and 1 - a, negative (-0 included) where that is 1 - a.
-__device__ __forceinline__ bool open(float s) { return (__float_as_uint(s) >> 31) != 0; }
+// A gate as one number that loses no precision for a near 0 or near 1: the
+// smaller of a and 1 - a, with the sign of the raw gate (positive, 0 included:
+// it is 1 - a).  `most`, the larger of the two, is what the gate still has at
+// hand where it is made.
+__device__ __forceinline__ bool open(float s) { return (int32_t)__float_as_uint(s) >= 0; }
 
-__device__ __forceinline__ float gate_of(float g) {
+__device__ __forceinline__ float gate_of(float g, float& most) {
     const float e = fast_exp2(fabsf(g) * -1.44269504088896340736f);
-    const float small = e * fast_rcp(1.0f + e);
-    return g >= 0.0f ? -small : small;   // (NaN stays NaN)
+    most = fast_rcp(1.0f + e);
+    return __builtin_copysignf(e * most, g);
 }
-__device__ __forceinline__ float take(float s) { return open(s) ? -s : 1.0f - s; }   // 1 - a
-constexpr float kKeepAll = -0.0f;                                                    // a = 1
+__device__ __forceinline__ float take(float s, float most) { return open(s) ? s : most; }   // 1 - a
 
-// a h.  For a near 1 it is h - (1 - a) h: the rounding of such an a (2^-24 of h
-// at every token) would add up over the gate's memory, 1 / (1 - a) tokens;
-// that of 1 - a does not.
-__device__ __forceinline__ float keep(float s, float h) { return fmaf(s, h, open(s) ? h : 0.0f); }
+// a h + in, in = l x.  For a near 1 it is h - (1 - a) h: the rounding of such an a
+// (2^-24 of h at every token) would add up over the gate's memory, 1 / (1 - a)
+// tokens; that of 1 - a does not.
+__device__ __forceinline__ float keep(float s, float h) { return fmaf(-s, h, open(s) ? h : 0.0f); }
+__device__ __forceinline__ float keep(float s, float h, float l, float x) {
+    return fmaf(-s, h, fmaf(l, x, open(s) ? h : 0.0f));
+}
+
+// Rows behind a wave's last token are made to change nothing: their gate is
+// +inf (a = 1) and their x (and lam) 0.
+__device__ __forceinline__ void no_row(uint16_t& gate, uint16_t& x) { gate = 0x7f80u, x = 0; }
+__device__ __forceinline__ void no_row(uint16_t& gate, uint32_t& x) { gate = 0x7f80u, x = 0; }
+__device__ __forceinline__ void no_row(uint32_t& gate, uint32_t& x) { gate = 0x7f807f80u, x = 0; }
+__device__ __forceinline__ void no_row(float& gate, float& x) { gate = __builtin_inff(), x = 0.0f; }
+
+// Loads above stay above (the scheduler would trade them for registers).
+__device__ __forceinline__ void loads_first() { __builtin_amdgcn_sched_barrier(0); }
 
 // ---------------------------------------------------------------- tiles' results
 // What a tile tells the tiles behind it about one channel, in one 64-bit word
@@ -89,64 +116,85 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The state that the `most` >= 1 tiles before this one (the words of tile i are
-// `stride` further each, i = 1 the nearest; the furthest is the sequence's
-// end) leave in front of it.  Every wave looks at one tile a round, kWaves tiles
-// further each round, until for each channel one of them has said its state;
-// from there the (A, B) of the nearer ones lead back, h -> A h + B one tile after
-// the other.  That is the arithmetic by which those tiles get their own states, so
-// the result does not depend on who was first.  Behind kWindow tiles without a
-// state the furthest are asked again: the first tile of a sequence waits for
-// nobody, so each one after it gets its state in turn.
+// A tile's flag says how far it is: a hint, so that those who wait read four
+// bytes a tile and not its words, which say the same by themselves.
+constexpr uint32_t kHasProduct = 1, kHasState = 2;
+
+__device__ __forceinline__ void raise(uint32_t* flag, uint32_t to) {
+    __hip_atomic_store(flag, to, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The state that the `most` >= 1 tiles before this one leave in front of it (tile
+// i's words are i strides further, i = 1 the nearest; the furthest is the
+// sequence's end).  One wave looks at the flags of the nearest kWindow tiles until
+// one has its state and all nearer ones their (A, B); the waves then fetch those
+// tiles' words, and from the state the (A, B) lead back, h -> A h + B one tile
+// after the other.  That is the arithmetic by which those tiles get their own
+// states, so the result does not depend on who was first.  Where the nearest
+// kWindow tiles have no state yet, one of them gets it in its turn: the first tile
+// of a sequence waits for nobody.
 constexpr int kWindow = 32;
+constexpr int kFetch = kWindow / kWaves;   // tiles that a wave fetches at most
 
 template <int V>
-__device__ __forceinline__ void look_back(const uint64_t* words, int64_t stride, int64_t most, int wave, int lane,
-                                          float2 (&board)[kWindow][V][64], float (&carry)[V]) {
-    int from[V];   // the nearest tile that said its state, 0: none yet
-#pragma unroll
-    for (int v = 0; v < V; ++v) from[v] = 0;
-    for (int first = 0;; first = first + kWaves < kWindow ? first + kWaves : first) {
-        const int64_t i = first + wave + 1;
-        if (i <= most) {
-            const uint64_t* p = words + i * stride;
-            uint64_t word[V];
-            for (;;) {
-                bool all = true;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    word[v] = peek(p + v);
-                    all = all && word[v] != kNothing;
+__device__ __forceinline__ void look_back(const uint64_t* words, int64_t stride, const uint32_t* flag,
+                                          int flag_stride, int64_t most, int wave, int lane,
+                                          float2 (&board)[kWindow][V][64], int* shared, float (&carry)[V]) {
+    if (wave == 0) {
+        const int in_reach = most < kWindow ? (int)most : kWindow;
+        for (;;) {
+            uint32_t f = 0;
+            if (lane < in_reach)
+                f = __hip_atomic_load(flag + (int64_t)(lane + 1) * flag_stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const uint64_t state = __ballot(f == kHasState), some = __ballot(f != 0);
+            if (state) {
+                const int nearest = __ffsll((unsigned long long)state) - 1;
+                const uint64_t nearer = ((uint64_t)1 << nearest) - 1;
+                if ((some & nearer) == nearer) {
+                    if (lane == 0) *shared = nearest + 1;
+                    break;
                 }
-                if (__all(all)) break;
-                __builtin_amdgcn_s_sleep(1);
             }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                // a sequence's furthest tile says its state; anything else there is an end too
-                const bool state = (uint32_t)(word[v] >> 32) == kState || i == most;
-                board[first + wave][v][lane] = make_float2(state ? -1.0f : __uint_as_float((uint32_t)(word[v] >> 32)),
-                                                           __uint_as_float((uint32_t)word[v]));
-            }
+            __builtin_amdgcn_s_sleep(1);
         }
-        __syncthreads();
-        bool every = true;
+    }
+    __syncthreads();
+    const int far = uniform(*shared);
+    uint64_t word[kFetch][V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            for (int k = first; k < first + kWaves && k < most; ++k)
-                if (!from[v] && board[k][v][lane].x == -1.0f) from[v] = k + 1;
-            every = every && from[v];
-        }
-        // the same in every wave: all of them read the same board
-        if (__all(every)) break;
-        __syncthreads();
+    for (int a = 0; a < kFetch; ++a) {
+        const int i = a * kWaves + wave + 1;
+        if (i <= far)
+#pragma unroll
+            for (int v = 0; v < V; ++v) word[a][v] = peek(words + i * stride + v);
     }
 #pragma unroll
+    for (int a = 0; a < kFetch; ++a) {
+        const int i = a * kWaves + wave + 1;
+        if (i <= far) {
+            for (;;) {   // a flag may be seen before its tile's words
+                bool all = true;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    all = all && (i < far ? word[a][v] != kNothing : (uint32_t)(word[a][v] >> 32) == kState);
+                if (__all(all)) break;
+                __builtin_amdgcn_s_sleep(1);
+#pragma unroll
+                for (int v = 0; v < V; ++v) word[a][v] = peek(words + i * stride + v);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                board[i - 1][v][lane] = make_float2(__uint_as_float((uint32_t)(word[a][v] >> 32)),
+                                                    __uint_as_float((uint32_t)word[a][v]));
+        }
+    }
+    __syncthreads();
+#pragma unroll
     for (int v = 0; v < V; ++v) {
-        float h = board[from[v] - 1][v][lane].y;
-        for (int k = from[v] - 2; k >= 0; --k) {
+        float h = board[far - 1][v][lane].y;   // a state
+        for (int k = far - 2; k >= 0; --k) {
             const float2 f = board[k][v][lane];
-            h = fmaf(f.x, h, f.y);
+            h = __float_as_uint(f.x) == kState ? f.y : fmaf(f.x, h, f.y);   // one may have got its state since
         }
         carry[v] = h;
     }
@@ -167,6 +215,7 @@ struct Launch {
     uint32_t tiles;         // of a sequence (rows of equal length), else of all
     uint32_t total;         // of all
     uint32_t* counters;     // NULL where no sequence can have two tiles
+    uint32_t* flags;        // [blocks][total]
     uint64_t* words;        // [total][D]
 };
 
@@ -176,6 +225,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch
     using RG = typename Raw<T, SHARED ? 1 : V>::type;
     __shared__ float2 parts[kWaves][V][64], board[kWindow][V][64];
     __shared__ uint32_t number;
+    __shared__ int far;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint32_t block = blockIdx.x % la.blocks;
     const uint32_t w = tile_number(la.counters, la.blocks, block, &number);
@@ -184,14 +234,19 @@ __global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch
     const int64_t d_own = (int64_t)block * (64 * V) + lane * V;
     const bool valid = d_own < D;
     const int64_t d = valid ? d_own : D - V;   // lanes behind the last channel read it and write nothing
+    const uint32_t dd = (uint32_t)d * sizeof(T);
     uint64_t* words = la.words + (size_t)w * D + d;
+    uint32_t* flag = la.flags + (size_t)block * la.total + w;
     const int64_t start = tile.j * kSeqTile;   // in the sequence
     T* __restrict__ y = static_cast<T*>(s.y);
 
     if (tile.n == s.N || (start >= tile.rows && start > 0)) {   // no tokens here
-        if (la.counters && wave == 0 && valid)
+        if (la.counters && wave == 0) {
+            if (valid)
 #pragma unroll
-            for (int v = 0; v < V; ++v) publish(words + v, kState, 0.0f);
+                for (int v = 0; v < V; ++v) publish(words + v, kState, 0.0f);
+            if (lane == 0) raise(flag, kHasState);
+        }
         if (tile.n == s.N && (s.flags & GSPN_SEQ_ZERO_TAIL) && valid) {
             const float zero[V] = {};
             for (int64_t t = start + wave; t < tile.rows && t < start + kSeqTile; t += kWaves)
@@ -209,32 +264,38 @@ __global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch
     for (int v = 0; v < V; ++v) p[v] = 1.0f, b[v] = 0.0f;
     if (count > 0) {
         const int64_t row = tile.row + start + wave * kTokens;
-        const int64_t k = SHARED ? d / s.ch_per_weight : d;
-        const T* __restrict__ gp = static_cast<const T*>(s.gate) + row * s.gate_stride;
-        const T* __restrict__ xp = static_cast<const T*>(s.x) + row * s.x_stride;
-        const T* __restrict__ lp = static_cast<const T*>(s.lam) + row * s.lam_stride;
-        const T* __restrict__ up = static_cast<const T*>(s.u) + row * s.u_stride;
+        const uint32_t dk = (SHARED ? (uint32_t)d / (uint32_t)s.ch_per_weight : (uint32_t)d) * sizeof(T);
+        Walk<T> gp(s.gate, row, s.gate_stride), xp(s.x, row, s.x_stride);
+        Walk<T> lp(s.lam, row, s.lam_stride), up(s.u, row, s.u_stride);
         RG gv[kTokens];
         R xv[kTokens], lv[kTokens];
 #pragma unroll
         for (int t = 0; t < kTokens; ++t) {
-            const int64_t i = t < count ? t : count - 1;   // rows behind the last read it again
-            gv[t] = *reinterpret_cast<const RG*>(gp + i * s.gate_stride + k);
-            xv[t] = *reinterpret_cast<const R*>(xp + i * s.x_stride + d);
-            if constexpr (LAM) lv[t] = *reinterpret_cast<const R*>(lp + i * s.lam_stride + d);
-            if constexpr (U) uv[t] = *reinterpret_cast<const R*>(up + i * s.u_stride + d);
+            gv[t] = gp.template at<RG>(dk);
+            xv[t] = xp.template at<R>(dd);
+            if constexpr (LAM) lv[t] = lp.template at<R>(dd);
+            if constexpr (U) uv[t] = up.template at<R>(dd);
+            const bool more = t + 1 < count;   // rows behind the last read it again
+            gp.down(more), xp.down(more);
+            if constexpr (LAM) lp.down(more);
+            if constexpr (U) up.down(more);
         }
+        loads_first();
+        if (count < kTokens)
+#pragma unroll
+            for (int t = 0; t < kTokens; ++t)
+                if (t >= count) {
+                    no_row(gv[t], xv[t]);
+                    if constexpr (LAM) lv[t] = R(0);
+                }
 #pragma unroll
         for (int t = 0; t < kTokens; ++t) {
-            float sg[V];
+            float sg = 0.0f, most = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (v == 0 || !SHARED) sg[v] = t < count ? gate_of(channel<SHARED ? 1 : V>(gv[t], v)) : kKeepAll;
-                else sg[v] = sg[0];
-                float in = (LAM ? channel<V>(lv[t], v) : take(sg[v])) * channel<V>(xv[t], v);
-                if (t >= count) in = 0.0f;
-                b[v] = keep(sg[v], b[v]) + in;
-                p[v] = keep(sg[v], p[v]);
+                if (v == 0 || !SHARED) sg = gate_of(channel<SHARED ? 1 : V>(gv[t], v), most);
+                b[v] = keep(sg, b[v], LAM ? channel<V>(lv[t], v) : take(sg, most), channel<V>(xv[t], v));
+                p[v] = keep(sg, p[v]);
                 h[t][v] = b[v];
                 P[t][v] = p[v];
             }
@@ -243,17 +304,24 @@ __global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch
 #pragma unroll
     for (int v = 0; v < V; ++v) parts[wave][v][lane] = make_float2(p[v], b[v]);
     __syncthreads();
-    // the stretch in front of this wave, and the whole tile
+    // the stretch in front of this wave, and (wave 0, which tells) the whole tile
     float pa[V], pb[V], ta[V], tb[V];
+    {
+        float2 f[kWaves][V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        ta[v] = 1.0f, tb[v] = 0.0f;
+        for (int k = 0; k < kWaves; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[k][v] = parts[k][v][lane];
+#pragma unroll
+        for (int v = 0; v < V; ++v) pa[v] = 1.0f, pb[v] = 0.0f, ta[v] = 1.0f, tb[v] = 0.0f;
 #pragma unroll
         for (int k = 0; k < kWaves; ++k) {
-            if (k == wave) pa[v] = ta[v], pb[v] = tb[v];
-            const float2 f = parts[k][v][lane];
-            tb[v] = fmaf(f.x, tb[v], f.y);
-            ta[v] *= f.x;
+            if (k < wave)
+#pragma unroll
+                for (int v = 0; v < V; ++v) pb[v] = fmaf(f[k][v].x, pb[v], f[k][v].y), pa[v] *= f[k][v].x;
+            if (wave == 0)
+#pragma unroll
+                for (int v = 0; v < V; ++v) tb[v] = fmaf(f[k][v].x, tb[v], f[k][v].y), ta[v] *= f[k][v].x;
         }
     }
     float carry[V];   // the state in front of the tile
@@ -261,10 +329,13 @@ __global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch
 #pragma unroll
         for (int v = 0; v < V; ++v) carry[v] = s.h0 ? s.h0[tile.n * D + d + v] : 0.0f;
     } else {
-        if (wave == 0 && valid)
+        if (wave == 0) {
+            if (valid)
 #pragma unroll
-            for (int v = 0; v < V; ++v) publish(words + v, product_bits(ta[v]), tb[v]);
-        look_back<V>(words, -D, tile.j, wave, lane, board, carry);
+                for (int v = 0; v < V; ++v) publish(words + v, product_bits(ta[v]), tb[v]);
+            if (lane == 0) raise(flag, kHasProduct);
+        }
+        look_back<V>(words, -D, flag, -1, tile.j, wave, lane, board, &far, carry);
     }
     if (wave == 0 && valid) {
 #pragma unroll
@@ -272,6 +343,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch
             if (la.counters) publish(words + v, kState, fmaf(ta[v], carry[v], tb[v]));
             if (s.states) s.states[(size_t)w * D + d + v] = carry[v];
         }
+        if (la.counters && lane == 0) raise(flag, kHasState);
     }
     if (s.h_last && wave == 0 && valid && start + kSeqTile >= tile.rows)
 #pragma unroll
@@ -279,21 +351,49 @@ __global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch
     if (!valid) return;
 #pragma unroll
     for (int v = 0; v < V; ++v) carry[v] = fmaf(pa[v], carry[v], pb[v]);
-    T* __restrict__ yp = y + (tile.row + start + wave * kTokens) * s.y_stride + d;
+    Walk<T> yp(s.y, tile.row + start + wave * kTokens, s.y_stride);
 #pragma unroll
     for (int t = 0; t < kTokens; ++t) {
-        if (t >= count) break;
-        float o[V];
+        if (t < count) {
+            float o[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            o[v] = fmaf(P[t][v], carry[v], h[t][v]);
-            if constexpr (U) o[v] *= channel<V>(uv[t], v);
+            for (int v = 0; v < V; ++v) {
+                o[v] = fmaf(P[t][v], carry[v], h[t][v]);
+                if constexpr (U) o[v] *= channel<V>(uv[t], v);
+            }
+            put(yp.out(dd), o);
         }
-        put(yp + t * s.y_stride, o);
+        yp.down();
     }
 }
 
 // ---------------------------------------------------------------- backward
+// v[t] of `lanes` (a power of two) neighbouring lanes added up; the last of them
+// has the sum.
+template <int CTRL> __device__ __forceinline__ float other(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int COUNT> __device__ __forceinline__ void add_lanes(float (&v)[COUNT], int lanes) {
+    if (lanes >= 2)
+#pragma unroll
+        for (int t = 0; t < COUNT; ++t) v[t] += other<0xb1>(v[t]);    // quad_perm [1, 0, 3, 2]
+    if (lanes >= 4)
+#pragma unroll
+        for (int t = 0; t < COUNT; ++t) v[t] += other<0x4e>(v[t]);    // quad_perm [2, 3, 0, 1]
+    if (lanes >= 8)
+#pragma unroll
+        for (int t = 0; t < COUNT; ++t) v[t] += other<0x141>(v[t]);   // row_half_mirror
+    if (lanes >= 16)
+#pragma unroll
+        for (int t = 0; t < COUNT; ++t) v[t] += other<0x140>(v[t]);   // row_mirror
+    if (lanes >= 32)
+#pragma unroll
+        for (int t = 0; t < COUNT; ++t) v[t] += other<0x142>(v[t]);   // row_bcast:15, into the next row
+    if (lanes >= 64)
+#pragma unroll
+        for (int t = 0; t < COUNT; ++t) v[t] += other<0x143>(v[t]);   // row_bcast:31, into the upper half
+}
+
 // The adjoint runs from a sequence's last tile to its first: with
 // R_t = a_t G_t the number that token t hands to token t - 1,
 // R_t = a_t (S_t + R_{t+1}), again R -> A R + B over a stretch.  The states
@@ -311,6 +411,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
     __shared__ float2 parts[kWaves][V][64], board[kWindow][V][64];
     __shared__ float back[kWaves][V][64];
     __shared__ uint32_t number;
+    __shared__ int far;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint32_t block = blockIdx.x % la.blocks;
     const uint32_t w = la.total - 1 - tile_number(la.counters, la.blocks, block, &number);
@@ -319,18 +420,24 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
     const int64_t d_own = (int64_t)block * (64 * V) + lane * V;
     const bool valid = d_own < D;
     const int64_t d = valid ? d_own : D - V;
+    const uint32_t dd = (uint32_t)d * sizeof(T);
     uint64_t* words = la.words + (size_t)w * D + d;
+    uint32_t* flag = la.flags + (size_t)block * la.total + w;
     const int64_t start = tile.j * kSeqTile;
-    const int64_t k = SHARED ? d / s.ch_per_weight : d;
+    const uint32_t k = SHARED ? (uint32_t)d / (uint32_t)s.ch_per_weight : (uint32_t)d;
+    const uint32_t dk = k * sizeof(T);
     T* __restrict__ gx = static_cast<T*>(g.gx);
     T* __restrict__ ggate = static_cast<T*>(g.ggate);
     T* __restrict__ glam = static_cast<T*>(g.glam);
     T* __restrict__ gu = static_cast<T*>(g.gu);
 
     if (tile.n == s.N || (start >= tile.rows && start > 0)) {
-        if (la.counters && wave == 0 && valid)
+        if (la.counters && wave == 0) {
+            if (valid)
 #pragma unroll
-            for (int v = 0; v < V; ++v) publish(words + v, kState, 0.0f);
+                for (int v = 0; v < V; ++v) publish(words + v, kState, 0.0f);
+            if (lane == 0) raise(flag, kHasState);
+        }
         if (tile.n == s.N && (s.flags & GSPN_SEQ_ZERO_TAIL) && valid) {
             const float zero[V] = {}, zero1[1] = {};
             for (int64_t t = start + wave; t < tile.rows && t < start + kSeqTile; t += kWaves) {
@@ -357,42 +464,50 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
     for (int v = 0; v < V; ++v) p[v] = 1.0f, b[v] = 0.0f, r[v] = 0.0f;
     // what the gradient of h_t is from y alone: u_t gy_t
     auto source = [&](int t, int v) {
-        const float q = g.gy ? channel<V>(gv[t], v) : 0.0f;
+        const float q = channel<V>(gv[t], v);
         return U ? q * channel<V>(uv[t], v) : q;
     };
     if (count > 0) {
-        const T* __restrict__ gp = static_cast<const T*>(s.gate) + row * s.gate_stride;
-        const T* __restrict__ xp = static_cast<const T*>(s.x) + row * s.x_stride;
-        const T* __restrict__ lp = static_cast<const T*>(s.lam) + row * s.lam_stride;
-        const T* __restrict__ up = static_cast<const T*>(s.u) + row * s.u_stride;
-        const T* __restrict__ yp = static_cast<const T*>(g.gy) + row * g.gy_stride;
+        Walk<T> gp(s.gate, row, s.gate_stride), xp(s.x, row, s.x_stride), yp(g.gy, row, g.gy_stride);
+        Walk<T> lp(s.lam, row, s.lam_stride), up(s.u, row, s.u_stride);
         RG raw[kTokens];
 #pragma unroll
         for (int t = 0; t < kTokens; ++t) {
-            const int64_t i = t < count ? t : count - 1;
-            raw[t] = *reinterpret_cast<const RG*>(gp + i * s.gate_stride + k);
-            xv[t] = *reinterpret_cast<const R*>(xp + i * s.x_stride + d);
-            if constexpr (LAM) lv[t] = *reinterpret_cast<const R*>(lp + i * s.lam_stride + d);
-            if constexpr (U) uv[t] = *reinterpret_cast<const R*>(up + i * s.u_stride + d);
-            if (g.gy) gv[t] = *reinterpret_cast<const R*>(yp + i * g.gy_stride + d);
+            raw[t] = gp.template at<RG>(dk);
+            xv[t] = xp.template at<R>(dd);
+            if constexpr (LAM) lv[t] = lp.template at<R>(dd);
+            if constexpr (U) uv[t] = up.template at<R>(dd);
+            gv[t] = R(0);
+            if (g.gy) gv[t] = yp.template at<R>(dd);
+            const bool more = t + 1 < count;   // rows behind the last read it again
+            gp.down(more), xp.down(more), yp.down(more);
+            if constexpr (LAM) lp.down(more);
+            if constexpr (U) up.down(more);
         }
+        loads_first();
+        if (count < kTokens)
+#pragma unroll
+            for (int t = 0; t < kTokens; ++t)
+                if (t >= count) {
+                    no_row(raw[t], xv[t]);
+                    gv[t] = R(0);
+                    if constexpr (LAM) lv[t] = R(0);
+                }
 #pragma unroll
         for (int t = 0; t < kTokens; ++t) {
+            float most = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (v == 0 || !SHARED) sg[t][v] = t < count ? gate_of(channel<SHARED ? 1 : V>(raw[t], v)) : kKeepAll;
+                if (v == 0 || !SHARED) sg[t][v] = gate_of(channel<SHARED ? 1 : V>(raw[t], v), most);
                 const float a = sg[t][SHARED ? 0 : v];
-                float in = (LAM ? channel<V>(lv[t], v) : take(a)) * channel<V>(xv[t], v);
-                if (t >= count) in = 0.0f;
-                b[v] = keep(a, b[v]) + in;
+                b[v] = keep(a, b[v], LAM ? channel<V>(lv[t], v) : take(a, most), channel<V>(xv[t], v));
                 p[v] = keep(a, p[v]);
             }
         }
 #pragma unroll
         for (int t = kTokens - 1; t >= 0; --t)
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (t < count) r[v] = keep(sg[t][SHARED ? 0 : v], source(t, v) + r[v]);
+            for (int v = 0; v < V; ++v) r[v] = keep(sg[t][SHARED ? 0 : v], source(t, v) + r[v]);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -401,22 +516,32 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
     }
     __syncthreads();
     float h0[V];                        // the state in front of this wave's tokens
-    float pa[V], pb[V], ta[V], tb[V];   // the adjoint's stretches: behind this wave, the whole tile
+    float pa[V], pb[V], ta[V], tb[V];   // the adjoint's stretches: behind this wave, (wave 0) the whole tile
+    {
+        float2 f[kWaves][V];
+        float e[kWaves][V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float f = s.states[(size_t)w * D + d + v];
+        for (int q = 0; q < kWaves; ++q)
 #pragma unroll
-        for (int q = 0; q < kWaves; ++q) {
-            if (q == wave) h0[v] = f;
-            f = fmaf(parts[q][v][lane].x, f, parts[q][v][lane].y);
+            for (int v = 0; v < V; ++v) f[q][v] = parts[q][v][lane], e[q][v] = back[q][v][lane];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            h0[v] = s.states[(size_t)w * D + d + v];
+            pa[v] = 1.0f, pb[v] = 0.0f, ta[v] = 1.0f, tb[v] = 0.0f;
         }
-        ta[v] = 1.0f, tb[v] = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kWaves; ++q)
+            if (q < wave)
+#pragma unroll
+                for (int v = 0; v < V; ++v) h0[v] = fmaf(f[q][v].x, h0[v], f[q][v].y);
 #pragma unroll
         for (int q = kWaves - 1; q >= 0; --q) {
-            if (q == wave) pa[v] = ta[v], pb[v] = tb[v];
-            const float a = parts[q][v][lane].x;
-            tb[v] = fmaf(a, tb[v], back[q][v][lane]);
-            ta[v] *= a;
+            if (q > wave)
+#pragma unroll
+                for (int v = 0; v < V; ++v) pb[v] = fmaf(f[q][v].x, pb[v], e[q][v]), pa[v] *= f[q][v].x;
+            if (wave == 0)
+#pragma unroll
+                for (int v = 0; v < V; ++v) tb[v] = fmaf(f[q][v].x, tb[v], e[q][v]), ta[v] *= f[q][v].x;
         }
     }
     float carry[V];   // what the token behind the tile hands to its last
@@ -425,10 +550,13 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
 #pragma unroll
         for (int v = 0; v < V; ++v) carry[v] = g.gh_last ? g.gh_last[tile.n * D + d + v] : 0.0f;
     } else {
-        if (wave == 0 && valid)
+        if (wave == 0) {
+            if (valid)
 #pragma unroll
-            for (int v = 0; v < V; ++v) publish(words + v, product_bits(ta[v]), tb[v]);
-        look_back<V>(words, D, behind, wave, lane, board, carry);
+                for (int v = 0; v < V; ++v) publish(words + v, product_bits(ta[v]), tb[v]);
+            if (lane == 0) raise(flag, kHasProduct);
+        }
+        look_back<V>(words, D, flag, 1, behind, wave, lane, board, &far, carry);
     }
     if (wave == 0 && valid) {
 #pragma unroll
@@ -437,6 +565,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
             if (la.counters) publish(words + v, kState, out);
             if (g.gh0 && tile.j == 0) g.gh0[tile.n * D + d + v] = out;
         }
+        if (la.counters && lane == 0) raise(flag, kHasState);
     }
     if (count <= 0) return;
     float h[kTokens + 1][V], G[V];
@@ -447,40 +576,62 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
 #pragma unroll
         for (int t = 0; t < kTokens; ++t) {
             const float a = sg[t][SHARED ? 0 : v];
-            h[t + 1][v] = keep(a, h[t][v]) + (LAM ? channel<V>(lv[t], v) : take(a)) * channel<V>(xv[t], v);
+            h[t + 1][v] = keep(a, h[t][v], LAM ? channel<V>(lv[t], v) : take(a, 1.0f + a), channel<V>(xv[t], v));
         }
     }
-    const int lanes = group / V;   // lanes of a group
+    float sum[SHARED ? kTokens : 1];   // a gate's gradient, of the lane's channels
+    {
+        const int64_t end = row + count - 1;   // the rows go up from the wave's last
+        Walk<T> ox(g.gx, end, g.gx_stride), ol(g.glam, end, g.glam_stride), ou(g.gu, end, g.gu_stride);
+        Walk<T> og(g.ggate, end, g.ggate_stride);
 #pragma unroll
-    for (int t = kTokens - 1; t >= 0; --t) {
-        if (t >= count) continue;
-        float ox[V], ol[V], ou[V], og[V];
+        for (int t = kTokens - 1; t >= 0; --t) {
+            if (t >= count) continue;
+            float vx[V], vl[V], vu[V], vg[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float a = sg[t][SHARED ? 0 : v];
-            const float x = channel<V>(xv[t], v), small = fabsf(a);
-            G[v] += source(t, v);
-            ox[v] = G[v] * (LAM ? channel<V>(lv[t], v) : take(a));
-            ol[v] = G[v] * x;
-            ou[v] = (g.gy ? channel<V>(gv[t], v) : 0.0f) * h[t + 1][v];
-            og[v] = small * (1.0f - small) * G[v] * (LAM ? h[t][v] : h[t][v] - x);
-            G[v] = keep(a, G[v]);
+            for (int v = 0; v < V; ++v) {
+                const float a = sg[t][SHARED ? 0 : v];
+                const float x = channel<V>(xv[t], v), small = fabsf(a);
+                G[v] += source(t, v);
+                vx[v] = G[v] * (LAM ? channel<V>(lv[t], v) : take(a, 1.0f + a));
+                vl[v] = G[v] * x;
+                vu[v] = channel<V>(gv[t], v) * h[t + 1][v];
+                vg[v] = fmaf(-small, small, small) * G[v] * (LAM ? h[t][v] : h[t][v] - x);
+                G[v] = keep(a, G[v]);
+            }
+            if (valid) {
+                if (g.gx) put(ox.out(dd), vx);
+                if (LAM && g.glam) put(ol.out(dd), vl);
+                if (U && g.gu) put(ou.out(dd), vu);
+                if (!SHARED && g.ggate) put(og.out(dd), vg);
+            }
+            ox.up(), ol.up(), ou.up(), og.up();
+            if constexpr (SHARED) {
+                sum[t] = vg[0];
+                if constexpr (V == 2) sum[t] += vg[1];
+            }
         }
-        const int64_t i = row + t;
-        if (valid) {
-            if (gx) put(gx + i * g.gx_stride + d, ox);
-            if (LAM && glam) put(glam + i * g.glam_stride + d, ol);
-            if (U && gu) put(gu + i * g.gu_stride + d, ou);
-        }
-        if constexpr (!SHARED) {
-            if (ggate && valid) put(ggate + i * g.ggate_stride + d, og);
-        } else if (ggate) {
-            float sum[1] = {og[0]};
-            if constexpr (V == 2) sum[0] += og[1];
-            for (int m = 1; m < lanes; m <<= 1) sum[0] += __shfl_xor(sum[0], m);
-            if (valid && lane % lanes == 0) {
-                if (partial) partial[i * (D / group) + d / group] = sum[0];
-                else put(ggate + i * g.ggate_stride + k, sum);
+    }
+    if constexpr (SHARED) {
+        if (!g.ggate) return;
+        const int lanes = group / V;   // of a group; its last one ends up with the sum
+        add_lanes(sum, lanes);
+        if (!valid || lane % lanes != lanes - 1) return;
+        if (partial) {
+            const int64_t width = D / group;
+            float* __restrict__ pp = partial + row * width + (uint32_t)d / (uint32_t)group;
+#pragma unroll
+            for (int t = 0; t < kTokens; ++t) {
+                if (t < count) *pp = sum[t];
+                pp += width;
+            }
+        } else {
+            Walk<T> og(g.ggate, row, g.ggate_stride);
+#pragma unroll
+            for (int t = 0; t < kTokens; ++t) {
+                const float one[1] = {sum[t]};
+                if (t < count) put(og.out(dk), one);
+                og.down();
             }
         }
     }
@@ -534,10 +685,11 @@ __global__ __launch_bounds__(256) void seq_step_kernel(gspn_seq_token s) {
     float h = s.state[slot * s.D + d];
     for (int64_t r = row; r < s.N; ++r) {
         if (r != row && s.slots[r] != slot) continue;
-        const float a = gate_of(to_f32(static_cast<const T*>(s.gate)[r * s.gate_stride + k]));
+        float most;
+        const float a = gate_of(to_f32(static_cast<const T*>(s.gate)[r * s.gate_stride + k]), most);
         const float xv = to_f32(static_cast<const T*>(s.x)[r * s.x_stride + d]);
-        const float lv = s.lam ? to_f32(static_cast<const T*>(s.lam)[r * s.lam_stride + d]) : take(a);
-        h = keep(a, h) + lv * xv;
+        const float lv = s.lam ? to_f32(static_cast<const T*>(s.lam)[r * s.lam_stride + d]) : take(a, most);
+        h = keep(a, h, lv, xv);
         const float uv = s.u ? to_f32(static_cast<const T*>(s.u)[r * s.u_stride + d]) : 1.0f;
         static_cast<T*>(s.y)[r * s.y_stride + d] = from_f32(uv * h, (T*)nullptr);
         if (!more) break;
@@ -551,7 +703,13 @@ bool tiles_wait(const gspn_seq& s) { return (s.offsets ? s.T : s.T / s.N) > kSeq
 
 int64_t counter_bytes(const gspn_seq& s) { return (s.D + 63) / 64 * 64; }   // 64 for the narrowest block
 
+int64_t flags_bytes(const gspn_seq& s) {
+    return ((s.D + 63) / 64 * total_tiles<kSeqTile>(s.offsets, s.T, s.N) * 4 + 15) / 16 * 16;
+}
+
 int64_t words_bytes(const gspn_seq& s) { return ((int64_t)total_tiles<kSeqTile>(s.offsets, s.T, s.N) * s.D * 8 + 15) / 16 * 16; }
+
+int64_t exchange_bytes(const gspn_seq& s) { return counter_bytes(s) + flags_bytes(s) + words_bytes(s); }
 
 int power_of_two_in(int64_t v, int most) {
     int p = 1;
@@ -575,17 +733,19 @@ Launch plan(const gspn_seq& s, int V) {
     la.tiles = s.offsets ? 0 : tiles_of_sequence<kSeqTile>(s.T, s.N);
     la.total = total_tiles<kSeqTile>(s.offsets, s.T, s.N);
     la.counters = nullptr;
+    la.flags = nullptr;
     la.words = nullptr;
     if (tiles_wait(s)) {
         la.counters = static_cast<uint32_t*>(s.work);
-        la.words = reinterpret_cast<uint64_t*>(static_cast<char*>(s.work) + counter_bytes(s));
+        la.flags = la.counters + counter_bytes(s) / 4;
+        la.words = reinterpret_cast<uint64_t*>(la.flags + flags_bytes(s) / 4);
     }
     return la;
 }
 
 void clear(const gspn_seq& s, const Launch& la, hipStream_t stream) {
     if (!la.counters) return;
-    const int64_t nc = counter_bytes(s) / 16, nw = words_bytes(s) / 16;
+    const int64_t nc = (counter_bytes(s) + flags_bytes(s)) / 16, nw = words_bytes(s) / 16;
     const unsigned grid = (unsigned)std::min<int64_t>((nc + nw + 255) / 256, 2048);
     hipLaunchKernelGGL(seq_clear_kernel, dim3(grid), dim3(256), 0, stream, reinterpret_cast<uint4*>(la.counters), nc,
                        reinterpret_cast<uint4*>(la.words), nw);
@@ -617,7 +777,7 @@ void bwd_variant(bool shared, bool lam, bool u, F f) {
 }  // namespace
 
 int64_t seq_workspace(const gspn_seq& s, bool backward) {
-    int64_t bytes = tiles_wait(s) ? counter_bytes(s) + words_bytes(s) : 0;
+    int64_t bytes = tiles_wait(s) ? exchange_bytes(s) : 0;
     const int group = power_of_two_in(s.ch_per_weight, 64);   // the smallest that a launch may take
     if (backward && group < s.ch_per_weight) bytes += s.T * (s.D / group) * 4;
     return bytes;
@@ -647,7 +807,7 @@ hipError_t launch_seq_bwd(const gspn_seq& s, const gspn_seq_grad& g, hipStream_t
     float* partial = nullptr;
     if (group < s.ch_per_weight && g.ggate)
         partial = reinterpret_cast<float*>(static_cast<char*>(s.work) +
-                                           (la.counters ? counter_bytes(s) + words_bytes(s) : 0));
+                                           (la.counters ? exchange_bytes(s) : 0));
     clear(s, la, stream);
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3(la.total * la.blocks), dim3(kWaves * 64), 0, stream, s, g, la, group, partial);
