@@ -420,9 +420,9 @@ int64_t gspn_block_rows(int64_t C_proxy, uint32_t dirs, int32_t ch_per_weight);
  * run side by side) need one each.
  */
 
-/* Flags of gspn_seq and gspn_adapter. */
+/* Flags of gspn_seq, gspn_seq_token and gspn_adapter. */
 enum {
-    GSPN_SEQ_ZERO_TAIL = 1 /* output rows behind the last sequence are set to zero */
+    GSPN_SEQ_ZERO_TAIL = 1 /* output rows of no sequence are set to zero */
 };
 
 typedef struct {
@@ -481,8 +481,8 @@ int64_t gspn_seq_states_rows(int64_t T, int64_t N);
  * One token for each of N requests, whose states live in a cache:
  *   state[s] = a state[s] + lam x   (or (1 - a) x),   y = u state[s],
  * s = slots[row] (slots NULL: row), in place.  A row whose slot is outside
- * [0, S) is skipped: it changes no state and its y is left as it was (a row of
- * padding takes slot -1).  Rows of the same slot are tokens of one request:
+ * [0, S) is skipped: it changes no state and its y is left as it was, or set to
+ * zero with GSPN_SEQ_ZERO_TAIL (a row of padding takes slot -1).  Rows of the same slot are tokens of one request:
  * they are taken one after the other, in the order of their rows.
  */
 typedef struct {
@@ -493,6 +493,7 @@ typedef struct {
     int64_t N, S, D;                /* N >= 0, S and D >= 1 */
     int64_t x_stride, gate_stride, lam_stride, u_stride, y_stride;
     int32_t ch_per_weight, dtype;
+    uint32_t flags;                 /* GSPN_SEQ_ZERO_TAIL or 0 */
 } gspn_seq_token;
 
 int gspn_seq_step(const gspn_seq_token *tok, hipStream_t stream);

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -58,7 +59,7 @@ class SeqToken(ctypes.Structure):
     _fields_ = ([(nm, ctypes.c_void_p) for nm in ("x", "gate", "lam", "u", "slots", "state", "y")]
                 + [(nm, ctypes.c_int64) for nm in ("N", "S", "D", "x_stride", "gate_stride", "lam_stride",
                                                    "u_stride", "y_stride")]
-                + [("ch_per_weight", ctypes.c_int32), ("dtype", ctypes.c_int32)])
+                + [("ch_per_weight", ctypes.c_int32), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)])
 
 
 class Adapter(ctypes.Structure):
@@ -67,6 +68,17 @@ class Adapter(ctypes.Structure):
                 + [(nm, ctypes.c_int64) for nm in ("work_bytes", "T", "K", "M", "N", "R", "r", "base_stride",
                                                    "x_stride", "out_stride")]
                 + [("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)])
+
+
+_CODES = {ctypes.c_void_p: "Q", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_uint32: "I"}
+
+
+def packer(cls):
+    """pack(*fields) -> the bytes of a cls, in one call (filling a ctypes struct costs one for every field).  A null
+    pointer is 0."""
+    fmt = struct.Struct("@" + "".join(_CODES[t] for _, t in cls._fields_) + "0Q")
+    assert fmt.size == ctypes.sizeof(cls)
+    return fmt.pack
 
 
 EXPORTED = ("gspn_scan_fwd", "gspn_scan_fwd_noalloc", "gspn_scan_fwd_path", "gspn_scan_fwd_ex", "gspn_scan_fwd_batched",
@@ -122,13 +134,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.gspn_block_fwd.restype = ctypes.c_int
         lib.gspn_block_rows.argtypes = [i64, u32, i32]
         lib.gspn_block_rows.restype = ctypes.c_int64
-        lib.gspn_seq_fwd.argtypes = [ctypes.POINTER(Seq), vp]
-        lib.gspn_seq_bwd.argtypes = [ctypes.POINTER(Seq), ctypes.POINTER(SeqGrad), vp]
-        lib.gspn_seq_step.argtypes = [ctypes.POINTER(SeqToken), vp]
-        lib.gspn_seq_workspace.argtypes = [ctypes.POINTER(Seq), i32]
+        # the structs go in by reference or as their bytes (pack)
+        lib.gspn_seq_fwd.argtypes = [vp, vp]
+        lib.gspn_seq_bwd.argtypes = [vp, vp, vp]
+        lib.gspn_seq_step.argtypes = [vp, vp]
+        lib.gspn_seq_workspace.argtypes = [vp, i32]
         lib.gspn_seq_states_rows.argtypes = [i64, i64]
-        lib.gspn_adapter_add.argtypes = [ctypes.POINTER(Adapter), vp]
-        lib.gspn_adapter_workspace.argtypes = [ctypes.POINTER(Adapter)]
+        lib.gspn_adapter_add.argtypes = [vp, vp]
+        lib.gspn_adapter_workspace.argtypes = [vp]
         for name in ("gspn_seq_fwd", "gspn_seq_bwd", "gspn_seq_step", "gspn_adapter_add"):
             getattr(lib, name).restype = ctypes.c_int
         for name in ("gspn_seq_workspace", "gspn_seq_states_rows", "gspn_adapter_workspace"):

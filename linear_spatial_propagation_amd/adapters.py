@@ -2,10 +2,10 @@
 (gspn_adapter_add of include/gspn.h)."""
 from __future__ import annotations
 
-import ctypes
-
 from . import _lib
-from .sequence import _call, _code, _index, _layout, _like, _output, _row_stride
+from .sequence import _call, _code, _index, _layout, _like, _row_stride
+
+_PACK = _lib.packer(_lib.Adapter)
 
 
 def adapter_add(base, x, a, b, ids, *, scale=None, offsets=None, out=None):
@@ -45,24 +45,24 @@ def adapter_add(base, x, a, b, ids, *, scale=None, offsets=None, out=None):
             raise ValueError(f"{name} must be contiguous")
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (base, x, a, b, scale)):
         raise RuntimeError("adapter_add has no backward; call it under torch.no_grad()")
-    s = _lib.Adapter(T=T, K=K, M=M, N=N, R=R, r=r, dtype=_code(x))
-    s.x, s.x_stride = x.data_ptr(), _row_stride("x", x)
-    s.base, s.base_stride = _like("base", base, x, x.shape[:-1] + (M,))
-    s.a, s.b = a.data_ptr(), b.data_ptr()
-    s.ids = _index("ids", ids, x.device)
-    if offsets is not None:
-        s.offsets = _index("offsets", offsets, x.device)
+    dev, code = x.device, _code(x)
+    px, sx = x.data_ptr(), _row_stride("x", x)
+    pb, sb = _like("base", base, x, x.shape[:-1] + (M,))
+    pi, po = _index("ids", ids, dev), _index("offsets", offsets, dev)
+    ps = 0
     if scale is not None:
-        if scale.device != x.device or scale.dtype != torch.float32 or scale.shape != (R,) or not scale.is_contiguous():
-            raise ValueError(f"scale must be a contiguous float32 tensor of {R} numbers on {x.device}")
-        s.scale = scale.data_ptr()
-    out, s.out, s.out_stride = _output("out", out, x, base.shape, s)
+        if scale.device != dev or scale.dtype != torch.float32 or scale.shape != (R,) or not scale.is_contiguous():
+            raise ValueError(f"scale must be a contiguous float32 tensor of {R} numbers on {dev}")
+        ps = scale.data_ptr()
+    flags = 0 if out is not None else _lib.SEQ_ZERO_TAIL
+    if out is None:
+        out = torch.empty(base.shape, dtype=x.dtype, device=dev)
+    py, sy = _like("out", out, x, base.shape)
     lib = _lib.load()
-    need = lib.gspn_adapter_workspace(ctypes.byref(s))
+    need = lib.gspn_adapter_workspace(_PACK(0, 0, 0, 0, 0, 0, po, 0, 0, 0, T, K, M, N, R, r, 0, 0, 0, code, 0))
     if need < 0:
         _lib.check(need)
-    if need:
-        work = torch.empty(need, dtype=torch.uint8, device=x.device)
-        s.work, s.work_bytes = work.data_ptr(), need
-    _call(lib.gspn_adapter_add, x.device, ctypes.byref(s))
+    work = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call(lib.gspn_adapter_add, dev, _PACK(pb, px, a.data_ptr(), b.data_ptr(), ps, pi, po, py, work.data_ptr(), need, T, K,
+                                           M, N, R, r, sb, sx, sy, code, flags))
     return out

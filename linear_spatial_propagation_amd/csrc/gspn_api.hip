@@ -610,7 +610,7 @@ int check_seq_sizes(int64_t T, int64_t D, int64_t N, int32_t cpw, int32_t dtype,
     if (check_dtype(dtype)) return GSPN_ERR_DTYPE;
     // 32-bit launches: at most one workgroup of 512 threads for a tile of
     // tokens, or a sequence's rest, and 64 channels
-    if ((T / gspn::kSeqTile + N + 1) * ((D + 63) / 64) > (1LL << 22)) return GSPN_ERR_SHAPE;
+    if (gspn::seq_tiles(T, N) * ((D + 63) / 64) > (1LL << 22)) return GSPN_ERR_SHAPE;
     return GSPN_OK;
 }
 
@@ -638,7 +638,7 @@ extern "C" {
 
 int64_t gspn_seq_states_rows(int64_t T, int64_t N) {
     if (T < 0 || N < 1 || T > kMaxTokens || N > kMaxTokens) return GSPN_ERR_SHAPE;
-    return T / gspn::kSeqTile + N;
+    return gspn::seq_states_rows(T, N);
 }
 
 int64_t gspn_seq_workspace(const gspn_seq* seq, int32_t backward) {
@@ -725,6 +725,7 @@ int gspn_seq_step(const gspn_seq_token* tok, hipStream_t stream) {
     if (t.N * ((t.D + 255) / 256) > (1LL << 22)) return GSPN_ERR_SHAPE;
     if (t.ch_per_weight < 1 || t.D % t.ch_per_weight) return GSPN_ERR_CPW;
     if (check_dtype(t.dtype)) return GSPN_ERR_DTYPE;
+    if (t.flags & ~(uint32_t)GSPN_SEQ_ZERO_TAIL) return GSPN_ERR_FLAGS;
     if (!t.state || (t.N > 0 && (!t.x || !t.gate || !t.y))) return GSPN_ERR_NULL;
     if (t.x_stride < 0 || t.gate_stride < 0 || t.lam_stride < 0 || t.u_stride < 0 ||
         rows_overlap(t.y, t.N, t.y_stride, t.D))

@@ -8,10 +8,10 @@
 //
 // A stretch of tokens maps the state in front of it to the state behind it by
 // h -> A h + B, A the product of its gates, and two stretches join to
-// (A2 A1, A2 B1 + B2).  So a sequence is cut into tiles of kSeqTile tokens
-// that work side by side:
+// (A2 A1, A2 B1 + B2).  So a sequence is cut into tiles that work side by
+// side:
 //  * a workgroup owns one tile of one block of channels (a lane owns V
-//    neighbouring channels), a wave kTokens tokens of it, held in registers:
+//    neighbouring channels), a wave TOKENS tokens of it, held in registers:
 //    every input is read once;
 //  * each wave forms its stretch's (A, B), the waves join theirs in LDS, and
 //    the workgroup publishes the tile's;
@@ -33,9 +33,6 @@
 
 namespace gspn {
 namespace {
-
-constexpr int kTokens = 16;                   // tokens of a wave
-constexpr int kWaves = kSeqTile / kTokens;    // waves of a workgroup
 
 // ---------------------------------------------------------------- rows
 // V neighbouring channels of a row as they are stored.
@@ -96,8 +93,9 @@ __device__ __forceinline__ void no_row(uint16_t& gate, uint32_t& x) { gate = 0x7
 __device__ __forceinline__ void no_row(uint32_t& gate, uint32_t& x) { gate = 0x7f807f80u, x = 0; }
 __device__ __forceinline__ void no_row(float& gate, float& x) { gate = __builtin_inff(), x = 0.0f; }
 
-// Loads above stay above (the scheduler would trade them for registers).
-__device__ __forceinline__ void loads_first() { __builtin_amdgcn_sched_barrier(0); }
+// The scheduler moves nothing across: loads above stay above, and what is below
+// does not take registers up there.
+__device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
 
 // ---------------------------------------------------------------- tiles' results
 // What a tile tells the tiles behind it about one channel, in one 64-bit word
@@ -126,22 +124,20 @@ __device__ __forceinline__ void raise(uint32_t* flag, uint32_t to) {
 
 // The state that the `most` >= 1 tiles before this one leave in front of it (tile
 // i's words are i strides further, i = 1 the nearest; the furthest is the
-// sequence's end).  One wave looks at the flags of the nearest kWindow tiles until
+// sequence's end).  One wave looks at the flags of the nearest WINDOW tiles until
 // one has its state and all nearer ones their (A, B); the waves then fetch those
 // tiles' words, and from the state the (A, B) lead back, h -> A h + B one tile
 // after the other.  That is the arithmetic by which those tiles get their own
 // states, so the result does not depend on who was first.  Where the nearest
-// kWindow tiles have no state yet, one of them gets it in its turn: the first tile
+// WINDOW tiles have no state yet, one of them gets it in its turn: the first tile
 // of a sequence waits for nobody.
-constexpr int kWindow = 32;
-constexpr int kFetch = kWindow / kWaves;   // tiles that a wave fetches at most
-
-template <int V>
+template <int V, int WAVES, int WINDOW>
 __device__ __forceinline__ void look_back(const uint64_t* words, int64_t stride, const uint32_t* flag,
                                           int flag_stride, int64_t most, int wave, int lane,
-                                          float2 (&board)[kWindow][V][64], int* shared, float (&carry)[V]) {
+                                          float2 (&board)[WINDOW][V][64], int* shared, float (&carry)[V]) {
+    constexpr int kFetch = WINDOW / WAVES;   // tiles that a wave fetches at most
     if (wave == 0) {
-        const int in_reach = most < kWindow ? (int)most : kWindow;
+        const int in_reach = most < WINDOW ? (int)most : WINDOW;
         for (;;) {
             uint32_t f = 0;
             if (lane < in_reach)
@@ -163,14 +159,14 @@ __device__ __forceinline__ void look_back(const uint64_t* words, int64_t stride,
     uint64_t word[kFetch][V];
 #pragma unroll
     for (int a = 0; a < kFetch; ++a) {
-        const int i = a * kWaves + wave + 1;
+        const int i = a * WAVES + wave + 1;
         if (i <= far)
 #pragma unroll
-            for (int v = 0; v < V; ++v) word[a][v] = peek(words + i * stride + v);
+            for (int v = 0; v < V; ++v) word[a][v] = peek(words + i * stride + v * 64);
     }
 #pragma unroll
     for (int a = 0; a < kFetch; ++a) {
-        const int i = a * kWaves + wave + 1;
+        const int i = a * WAVES + wave + 1;
         if (i <= far) {
             for (;;) {   // a flag may be seen before its tile's words
                 bool all = true;
@@ -180,7 +176,7 @@ __device__ __forceinline__ void look_back(const uint64_t* words, int64_t stride,
                 if (__all(all)) break;
                 __builtin_amdgcn_s_sleep(1);
 #pragma unroll
-                for (int v = 0; v < V; ++v) word[a][v] = peek(words + i * stride + v);
+                for (int v = 0; v < V; ++v) word[a][v] = peek(words + i * stride + v * 64);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v)
@@ -200,77 +196,91 @@ __device__ __forceinline__ void look_back(const uint64_t* words, int64_t stride,
     }
 }
 
-// The workgroup's tile: from the counter where tiles wait for each other.
-__device__ __forceinline__ uint32_t tile_number(uint32_t* __restrict__ counters, uint32_t blocks, uint32_t block,
-                                                uint32_t* shared) {
-    if (!counters) return blockIdx.x / blocks;
-    if (threadIdx.x == 0) *shared = atomicAdd(counters + block * 16, 1u);
-    __syncthreads();
-    return uniform(*shared);
-}
-
-// ---------------------------------------------------------------- forward
 struct Launch {
     uint32_t blocks;        // blocks of channels
-    uint32_t tiles;         // of a sequence (rows of equal length), else of all
+    uint32_t tiles;         // of a sequence (rows of equal length), else 0
     uint32_t total;         // of all
     uint32_t* counters;     // NULL where no sequence can have two tiles
     uint32_t* flags;        // [blocks][total]
-    uint64_t* words;        // [total][D]
+    uint64_t* words;        // [total][blocks][V][64]: a lane's channels 64 words apart, so that each is one whole line's
+    int spacing;            // tokens between two saved states
 };
 
-template <typename T, int V, bool SHARED, bool LAM, bool U>
-__global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch la) {
+// Tokens between two saved states: of long sequences 128, of many short ones 32.
+// It goes by T and N alone, as `states` is sized before anything else is known.
+inline int spacing_of(int64_t T, int64_t N) { return T <= 32 * N ? 32 : 128; }
+
+// The workgroup's tile: from the counter where tiles wait for each other.  Rows of
+// equal length are taken tile by tile across the sequences (the backward: from
+// the last), so that the tile in front of one's own was taken long ago.
+__device__ __forceinline__ uint32_t tile_number(const Launch& la, uint32_t block, bool from_last, uint32_t* shared) {
+    uint32_t k;
+    if (!la.counters) {
+        k = blockIdx.x / la.blocks;
+    } else {
+        if (threadIdx.x == 0) *shared = atomicAdd(la.counters + block * 16, 1u);
+        __syncthreads();
+        k = uniform(*shared);
+    }
+    if (from_last) k = la.total - 1 - k;
+    if (la.tiles == 0) return k;
+    const uint32_t sequences = la.total / la.tiles;
+    return (k % sequences) * la.tiles + k / sequences;
+}
+
+// ---------------------------------------------------------------- forward
+template <typename T, int V, bool SHARED, bool LAM, bool U, int TOKENS, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 2) void seq_fwd_kernel(gspn_seq s, Launch la) {
+    constexpr int TILE = TOKENS * WAVES, WINDOW = 4 * WAVES;
     using R = typename Raw<T, V>::type;
     using RG = typename Raw<T, SHARED ? 1 : V>::type;
-    __shared__ float2 parts[kWaves][V][64], board[kWindow][V][64];
+    __shared__ float2 parts[WAVES][V][64], board[WINDOW][V][64];
     __shared__ uint32_t number;
     __shared__ int far;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint32_t block = blockIdx.x % la.blocks;
-    const uint32_t w = tile_number(la.counters, la.blocks, block, &number);
-    const Tile tile = find_tile<kSeqTile>(s.offsets, s.T, s.N, la.tiles, w, lane);
+    const uint32_t w = tile_number(la, block, false, &number);
+    const Tile tile = find_tile<TILE>(s.offsets, s.T, s.N, la.tiles, w, lane);
     const int64_t D = s.D;
     const int64_t d_own = (int64_t)block * (64 * V) + lane * V;
     const bool valid = d_own < D;
     const int64_t d = valid ? d_own : D - V;   // lanes behind the last channel read it and write nothing
     const uint32_t dd = (uint32_t)d * sizeof(T);
-    uint64_t* words = la.words + (size_t)w * D + d;
+    uint64_t* words = la.words + ((size_t)w * la.blocks + block) * (64 * V) + lane;
     uint32_t* flag = la.flags + (size_t)block * la.total + w;
-    const int64_t start = tile.j * kSeqTile;   // in the sequence
+    const int64_t start = tile.j * TILE;   // in the sequence
     T* __restrict__ y = static_cast<T*>(s.y);
 
     if (tile.n == s.N || (start >= tile.rows && start > 0)) {   // no tokens here
         if (la.counters && wave == 0) {
-            if (valid)
 #pragma unroll
-                for (int v = 0; v < V; ++v) publish(words + v, kState, 0.0f);
+            for (int v = 0; v < V; ++v) publish(words + v * 64, kState, 0.0f);
             if (lane == 0) raise(flag, kHasState);
         }
         if (tile.n == s.N && (s.flags & GSPN_SEQ_ZERO_TAIL) && valid) {
             const float zero[V] = {};
-            for (int64_t t = start + wave; t < tile.rows && t < start + kSeqTile; t += kWaves)
+            for (int64_t t = start + wave; t < tile.rows && t < start + TILE; t += WAVES)
                 put(y + (tile.row + t) * s.y_stride + d, zero);
         }
         return;
     }
 
-    const int64_t left = tile.rows - start - wave * kTokens;
-    const int count = uniform((int)(left < 0 ? 0 : left < kTokens ? left : kTokens));   // tokens of this wave
-    float h[kTokens][V], P[kTokens][V];   // state and product of gates from the wave's first token on
-    R uv[kTokens];
+    const int64_t left = tile.rows - start - wave * TOKENS;
+    const int count = uniform((int)(left < 0 ? 0 : left < TOKENS ? left : TOKENS));   // tokens of this wave
+    float h[TOKENS][V], P[TOKENS][V];   // state and product of gates from the wave's first token on
+    R uv[TOKENS];
     float p[V], b[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) p[v] = 1.0f, b[v] = 0.0f;
     if (count > 0) {
-        const int64_t row = tile.row + start + wave * kTokens;
+        const int64_t row = tile.row + start + wave * TOKENS;
         const uint32_t dk = (SHARED ? (uint32_t)d / (uint32_t)s.ch_per_weight : (uint32_t)d) * sizeof(T);
         Walk<T> gp(s.gate, row, s.gate_stride), xp(s.x, row, s.x_stride);
         Walk<T> lp(s.lam, row, s.lam_stride), up(s.u, row, s.u_stride);
-        RG gv[kTokens];
-        R xv[kTokens], lv[kTokens];
+        RG gv[TOKENS];
+        R xv[TOKENS], lv[TOKENS];
 #pragma unroll
-        for (int t = 0; t < kTokens; ++t) {
+        for (int t = 0; t < TOKENS; ++t) {
             gv[t] = gp.template at<RG>(dk);
             xv[t] = xp.template at<R>(dd);
             if constexpr (LAM) lv[t] = lp.template at<R>(dd);
@@ -280,16 +290,16 @@ __global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch
             if constexpr (LAM) lp.down(more);
             if constexpr (U) up.down(more);
         }
-        loads_first();
-        if (count < kTokens)
+        hold();
+        if (count < TOKENS)
 #pragma unroll
-            for (int t = 0; t < kTokens; ++t)
+            for (int t = 0; t < TOKENS; ++t)
                 if (t >= count) {
                     no_row(gv[t], xv[t]);
                     if constexpr (LAM) lv[t] = R(0);
                 }
 #pragma unroll
-        for (int t = 0; t < kTokens; ++t) {
+        for (int t = 0; t < TOKENS; ++t) {
             float sg = 0.0f, most = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -299,6 +309,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch
                 h[t][v] = b[v];
                 P[t][v] = p[v];
             }
+            if (t % 2) hold();
         }
     }
 #pragma unroll
@@ -306,23 +317,18 @@ __global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch
     __syncthreads();
     // the stretch in front of this wave, and (wave 0, which tells) the whole tile
     float pa[V], pb[V], ta[V], tb[V];
-    {
-        float2 f[kWaves][V];
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k)
+    for (int v = 0; v < V; ++v) {
+        float2 f[WAVES];
 #pragma unroll
-            for (int v = 0; v < V; ++v) f[k][v] = parts[k][v][lane];
+        for (int k = 0; k < WAVES; ++k) f[k] = parts[k][v][lane];
+        pa[v] = 1.0f, pb[v] = 0.0f, ta[v] = 1.0f, tb[v] = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) pa[v] = 1.0f, pb[v] = 0.0f, ta[v] = 1.0f, tb[v] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kWaves; ++k) {
-            if (k < wave)
-#pragma unroll
-                for (int v = 0; v < V; ++v) pb[v] = fmaf(f[k][v].x, pb[v], f[k][v].y), pa[v] *= f[k][v].x;
-            if (wave == 0)
-#pragma unroll
-                for (int v = 0; v < V; ++v) tb[v] = fmaf(f[k][v].x, tb[v], f[k][v].y), ta[v] *= f[k][v].x;
+        for (int k = 0; k < WAVES; ++k) {
+            if (k < wave) pb[v] = fmaf(f[k].x, pb[v], f[k].y), pa[v] *= f[k].x;
+            if (wave == 0) tb[v] = fmaf(f[k].x, tb[v], f[k].y), ta[v] *= f[k].x;
         }
+        hold();
     }
     float carry[V];   // the state in front of the tile
     if (tile.j == 0) {
@@ -330,30 +336,36 @@ __global__ __launch_bounds__(kWaves * 64) void seq_fwd_kernel(gspn_seq s, Launch
         for (int v = 0; v < V; ++v) carry[v] = s.h0 ? s.h0[tile.n * D + d + v] : 0.0f;
     } else {
         if (wave == 0) {
-            if (valid)
 #pragma unroll
-                for (int v = 0; v < V; ++v) publish(words + v, product_bits(ta[v]), tb[v]);
+            for (int v = 0; v < V; ++v) publish(words + v * 64, product_bits(ta[v]), tb[v]);
             if (lane == 0) raise(flag, kHasProduct);
         }
-        look_back<V>(words, -D, flag, -1, tile.j, wave, lane, board, &far, carry);
+        look_back<V, WAVES, WINDOW>(words, -(int64_t)la.blocks * (64 * V), flag, -1, tile.j, wave, lane, board, &far, carry);
     }
-    if (wave == 0 && valid) {
+    if (wave == 0) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if (la.counters) publish(words + v, kState, fmaf(ta[v], carry[v], tb[v]));
-            if (s.states) s.states[(size_t)w * D + d + v] = carry[v];
+            if (la.counters) publish(words + v * 64, kState, fmaf(ta[v], carry[v], tb[v]));
         }
         if (la.counters && lane == 0) raise(flag, kHasState);
     }
-    if (s.h_last && wave == 0 && valid && start + kSeqTile >= tile.rows)
+    if (s.h_last && wave == 0 && valid && start + TILE >= tile.rows)
 #pragma unroll
         for (int v = 0; v < V; ++v) s.h_last[tile.n * D + d + v] = fmaf(ta[v], carry[v], tb[v]);
     if (!valid) return;
 #pragma unroll
     for (int v = 0; v < V; ++v) carry[v] = fmaf(pa[v], carry[v], pb[v]);
-    Walk<T> yp(s.y, tile.row + start + wave * kTokens, s.y_stride);
+    const int64_t first = start + wave * TOKENS;
+    if (s.states && first % la.spacing == 0 && (first == 0 || first < tile.rows)) {
+        // sequences take rows of `states` as they take tiles (find_tile)
+        const int64_t per = (tile.rows + la.spacing - 1) / la.spacing;
+        const int64_t at = (s.offsets ? tile.row / la.spacing + tile.n : tile.n * (per > 0 ? per : 1)) + first / la.spacing;
 #pragma unroll
-    for (int t = 0; t < kTokens; ++t) {
+        for (int v = 0; v < V; ++v) s.states[at * D + d + v] = carry[v];
+    }
+    Walk<T> yp(s.y, tile.row + start + wave * TOKENS, s.y_stride);
+#pragma unroll
+    for (int t = 0; t < TOKENS; ++t) {
         if (t < count) {
             float o[V];
 #pragma unroll
@@ -403,27 +415,28 @@ template <int COUNT> __device__ __forceinline__ void add_lanes(float (&v)[COUNT]
 // groups of `group` of them (the largest power of two that divides
 // ch_per_weight, at most a wave's channels) and writes the gradient, or, where
 // a set has more, the group's part for reduce_gate_kernel.
-template <typename T, int V, bool SHARED, bool LAM, bool U>
-__global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_seq_grad g, Launch la, int group,
-                                                              float* __restrict__ partial) {
+template <typename T, int V, bool SHARED, bool LAM, bool U, int TOKENS, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void seq_bwd_kernel(gspn_seq s, gspn_seq_grad g, Launch la, int group,
+                                                             float* __restrict__ partial) {
+    constexpr int TILE = TOKENS * WAVES, WINDOW = 4 * WAVES;   // TILE is the states' spacing
     using R = typename Raw<T, V>::type;
     using RG = typename Raw<T, SHARED ? 1 : V>::type;
-    __shared__ float2 parts[kWaves][V][64], board[kWindow][V][64];
-    __shared__ float back[kWaves][V][64];
+    __shared__ float2 parts[WAVES][V][64], board[WINDOW][V][64];
+    __shared__ float back[WAVES][V][64];
     __shared__ uint32_t number;
     __shared__ int far;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint32_t block = blockIdx.x % la.blocks;
-    const uint32_t w = la.total - 1 - tile_number(la.counters, la.blocks, block, &number);
-    const Tile tile = find_tile<kSeqTile>(s.offsets, s.T, s.N, la.tiles, w, lane);
+    const uint32_t w = tile_number(la, block, true, &number);
+    const Tile tile = find_tile<TILE>(s.offsets, s.T, s.N, la.tiles, w, lane);
     const int64_t D = s.D;
     const int64_t d_own = (int64_t)block * (64 * V) + lane * V;
     const bool valid = d_own < D;
     const int64_t d = valid ? d_own : D - V;
     const uint32_t dd = (uint32_t)d * sizeof(T);
-    uint64_t* words = la.words + (size_t)w * D + d;
+    uint64_t* words = la.words + ((size_t)w * la.blocks + block) * (64 * V) + lane;
     uint32_t* flag = la.flags + (size_t)block * la.total + w;
-    const int64_t start = tile.j * kSeqTile;
+    const int64_t start = tile.j * TILE;
     const uint32_t k = SHARED ? (uint32_t)d / (uint32_t)s.ch_per_weight : (uint32_t)d;
     const uint32_t dk = k * sizeof(T);
     T* __restrict__ gx = static_cast<T*>(g.gx);
@@ -433,14 +446,13 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
 
     if (tile.n == s.N || (start >= tile.rows && start > 0)) {
         if (la.counters && wave == 0) {
-            if (valid)
 #pragma unroll
-                for (int v = 0; v < V; ++v) publish(words + v, kState, 0.0f);
+            for (int v = 0; v < V; ++v) publish(words + v * 64, kState, 0.0f);
             if (lane == 0) raise(flag, kHasState);
         }
         if (tile.n == s.N && (s.flags & GSPN_SEQ_ZERO_TAIL) && valid) {
             const float zero[V] = {}, zero1[1] = {};
-            for (int64_t t = start + wave; t < tile.rows && t < start + kSeqTile; t += kWaves) {
+            for (int64_t t = start + wave; t < tile.rows && t < start + TILE; t += WAVES) {
                 const int64_t row = tile.row + t;
                 if (gx) put(gx + row * g.gx_stride + d, zero);
                 if (LAM && glam) put(glam + row * g.glam_stride + d, zero);
@@ -454,11 +466,11 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
         return;
     }
 
-    const int64_t left = tile.rows - start - wave * kTokens;
-    const int count = uniform((int)(left < 0 ? 0 : left < kTokens ? left : kTokens));
-    const int64_t row = tile.row + start + wave * kTokens;
-    float sg[kTokens][SHARED ? 1 : V];
-    R xv[kTokens], lv[kTokens], uv[kTokens], gv[kTokens];
+    const int64_t left = tile.rows - start - wave * TOKENS;
+    const int count = uniform((int)(left < 0 ? 0 : left < TOKENS ? left : TOKENS));
+    const int64_t row = tile.row + start + wave * TOKENS;
+    float sg[TOKENS][SHARED ? 1 : V];
+    R xv[TOKENS], lv[TOKENS], uv[TOKENS], gv[TOKENS];
     float p[V], b[V], r[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) p[v] = 1.0f, b[v] = 0.0f, r[v] = 0.0f;
@@ -470,9 +482,9 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
     if (count > 0) {
         Walk<T> gp(s.gate, row, s.gate_stride), xp(s.x, row, s.x_stride), yp(g.gy, row, g.gy_stride);
         Walk<T> lp(s.lam, row, s.lam_stride), up(s.u, row, s.u_stride);
-        RG raw[kTokens];
+        RG raw[TOKENS];
 #pragma unroll
-        for (int t = 0; t < kTokens; ++t) {
+        for (int t = 0; t < TOKENS; ++t) {
             raw[t] = gp.template at<RG>(dk);
             xv[t] = xp.template at<R>(dd);
             if constexpr (LAM) lv[t] = lp.template at<R>(dd);
@@ -484,17 +496,17 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
             if constexpr (LAM) lp.down(more);
             if constexpr (U) up.down(more);
         }
-        loads_first();
-        if (count < kTokens)
+        hold();
+        if (count < TOKENS)
 #pragma unroll
-            for (int t = 0; t < kTokens; ++t)
+            for (int t = 0; t < TOKENS; ++t)
                 if (t >= count) {
                     no_row(raw[t], xv[t]);
                     gv[t] = R(0);
                     if constexpr (LAM) lv[t] = R(0);
                 }
 #pragma unroll
-        for (int t = 0; t < kTokens; ++t) {
+        for (int t = 0; t < TOKENS; ++t) {
             float most = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -505,7 +517,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
             }
         }
 #pragma unroll
-        for (int t = kTokens - 1; t >= 0; --t)
+        for (int t = TOKENS - 1; t >= 0; --t)
 #pragma unroll
             for (int v = 0; v < V; ++v) r[v] = keep(sg[t][SHARED ? 0 : v], source(t, v) + r[v]);
     }
@@ -518,10 +530,10 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
     float h0[V];                        // the state in front of this wave's tokens
     float pa[V], pb[V], ta[V], tb[V];   // the adjoint's stretches: behind this wave, (wave 0) the whole tile
     {
-        float2 f[kWaves][V];
-        float e[kWaves][V];
+        float2 f[WAVES][V];
+        float e[WAVES][V];
 #pragma unroll
-        for (int q = 0; q < kWaves; ++q)
+        for (int q = 0; q < WAVES; ++q)
 #pragma unroll
             for (int v = 0; v < V; ++v) f[q][v] = parts[q][v][lane], e[q][v] = back[q][v][lane];
 #pragma unroll
@@ -530,12 +542,12 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
             pa[v] = 1.0f, pb[v] = 0.0f, ta[v] = 1.0f, tb[v] = 0.0f;
         }
 #pragma unroll
-        for (int q = 0; q < kWaves; ++q)
+        for (int q = 0; q < WAVES; ++q)
             if (q < wave)
 #pragma unroll
                 for (int v = 0; v < V; ++v) h0[v] = fmaf(f[q][v].x, h0[v], f[q][v].y);
 #pragma unroll
-        for (int q = kWaves - 1; q >= 0; --q) {
+        for (int q = WAVES - 1; q >= 0; --q) {
             if (q > wave)
 #pragma unroll
                 for (int v = 0; v < V; ++v) pb[v] = fmaf(f[q][v].x, pb[v], e[q][v]), pa[v] *= f[q][v].x;
@@ -545,47 +557,46 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
         }
     }
     float carry[V];   // what the token behind the tile hands to its last
-    const int64_t behind = (tile.rows + kSeqTile - 1) / kSeqTile - 1 - tile.j;
+    const int64_t behind = (tile.rows + TILE - 1) / TILE - 1 - tile.j;
     if (behind <= 0) {
 #pragma unroll
         for (int v = 0; v < V; ++v) carry[v] = g.gh_last ? g.gh_last[tile.n * D + d + v] : 0.0f;
     } else {
         if (wave == 0) {
-            if (valid)
 #pragma unroll
-                for (int v = 0; v < V; ++v) publish(words + v, product_bits(ta[v]), tb[v]);
+            for (int v = 0; v < V; ++v) publish(words + v * 64, product_bits(ta[v]), tb[v]);
             if (lane == 0) raise(flag, kHasProduct);
         }
-        look_back<V>(words, D, flag, 1, behind, wave, lane, board, &far, carry);
+        look_back<V, WAVES, WINDOW>(words, (int64_t)la.blocks * (64 * V), flag, 1, behind, wave, lane, board, &far, carry);
     }
-    if (wave == 0 && valid) {
+    if (wave == 0) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const float out = fmaf(ta[v], carry[v], tb[v]);
-            if (la.counters) publish(words + v, kState, out);
-            if (g.gh0 && tile.j == 0) g.gh0[tile.n * D + d + v] = out;
+            if (la.counters) publish(words + v * 64, kState, out);
+            if (g.gh0 && valid && tile.j == 0) g.gh0[tile.n * D + d + v] = out;
         }
         if (la.counters && lane == 0) raise(flag, kHasState);
     }
     if (count <= 0) return;
-    float h[kTokens + 1][V], G[V];
+    float h[TOKENS + 1][V], G[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         G[v] = fmaf(pa[v], carry[v], pb[v]);   // R of the token behind
         h[0][v] = h0[v];
 #pragma unroll
-        for (int t = 0; t < kTokens; ++t) {
+        for (int t = 0; t < TOKENS; ++t) {
             const float a = sg[t][SHARED ? 0 : v];
             h[t + 1][v] = keep(a, h[t][v], LAM ? channel<V>(lv[t], v) : take(a, 1.0f + a), channel<V>(xv[t], v));
         }
     }
-    float sum[SHARED ? kTokens : 1];   // a gate's gradient, of the lane's channels
+    float sum[SHARED ? TOKENS : 1];   // a gate's gradient, of the lane's channels
     {
         const int64_t end = row + count - 1;   // the rows go up from the wave's last
         Walk<T> ox(g.gx, end, g.gx_stride), ol(g.glam, end, g.glam_stride), ou(g.gu, end, g.gu_stride);
         Walk<T> og(g.ggate, end, g.ggate_stride);
 #pragma unroll
-        for (int t = kTokens - 1; t >= 0; --t) {
+        for (int t = TOKENS - 1; t >= 0; --t) {
             if (t >= count) continue;
             float vx[V], vl[V], vu[V], vg[V];
 #pragma unroll
@@ -621,14 +632,14 @@ __global__ __launch_bounds__(kWaves * 64) void seq_bwd_kernel(gspn_seq s, gspn_s
             const int64_t width = D / group;
             float* __restrict__ pp = partial + row * width + (uint32_t)d / (uint32_t)group;
 #pragma unroll
-            for (int t = 0; t < kTokens; ++t) {
+            for (int t = 0; t < TOKENS; ++t) {
                 if (t < count) *pp = sum[t];
                 pp += width;
             }
         } else {
             Walk<T> og(g.ggate, row, g.ggate_stride);
 #pragma unroll
-            for (int t = 0; t < kTokens; ++t) {
+            for (int t = 0; t < TOKENS; ++t) {
                 const float one[1] = {sum[t]};
                 if (t < count) put(og.out(dk), one);
                 og.down();
@@ -671,7 +682,11 @@ __global__ __launch_bounds__(256) void seq_step_kernel(gspn_seq_token s) {
     const int64_t row = blockIdx.x / blocks;
     const int64_t d = (blockIdx.x - row * blocks) * 256 + threadIdx.x;
     const int64_t slot = s.slots ? s.slots[row] : row;
-    if (slot < 0 || slot >= s.S) return;
+    if (slot < 0 || slot >= s.S) {
+        if ((s.flags & GSPN_SEQ_ZERO_TAIL) && d < s.D)
+            static_cast<T*>(s.y)[row * s.y_stride + d] = from_f32(0.0f, (T*)nullptr);
+        return;
+    }
     bool more = false;
     if (s.slots) {
         bool earlier = false, later = false;
@@ -698,18 +713,39 @@ __global__ __launch_bounds__(256) void seq_step_kernel(gspn_seq_token s) {
 }
 
 // ---------------------------------------------------------------- host
-// Whether a sequence may have two tiles.
-bool tiles_wait(const gspn_seq& s) { return (s.offsets ? s.T : s.T / s.N) > kSeqTile; }
+// Forward tiles are 256 tokens (eight waves of 32): the fewer tiles, the fewer
+// wait for each other.  The backward holds more for a token and takes 128 (eight
+// of 16).  Many short sequences would leave most waves of such tiles without a
+// token: theirs are 32 (four waves of 8).
+bool short_sequences(const gspn_seq& s) { return spacing_of(s.T, s.N) == 32; }
 
-int64_t counter_bytes(const gspn_seq& s) { return (s.D + 63) / 64 * 64; }   // 64 for the narrowest block
+int tile_of(const gspn_seq& s, bool backward) { return short_sequences(s) ? 32 : backward ? 128 : 256; }
 
-int64_t flags_bytes(const gspn_seq& s) {
-    return ((s.D + 63) / 64 * total_tiles<kSeqTile>(s.offsets, s.T, s.N) * 4 + 15) / 16 * 16;
+uint32_t tiles_of_sequence(const gspn_seq& s, int tile) {
+    const int64_t rows = s.T / s.N;
+    return (uint32_t)(rows > 0 ? (rows + tile - 1) / tile : 1);
+}
+uint32_t total_tiles(const gspn_seq& s, int tile) {
+    return s.offsets ? (uint32_t)(s.T / tile + s.N + 1) : (uint32_t)s.N * tiles_of_sequence(s, tile);
 }
 
-int64_t words_bytes(const gspn_seq& s) { return ((int64_t)total_tiles<kSeqTile>(s.offsets, s.T, s.N) * s.D * 8 + 15) / 16 * 16; }
+// Whether a sequence may have two tiles.
+bool tiles_wait(const gspn_seq& s, int tile) { return (s.offsets ? s.T : s.T / s.N) > tile; }
 
-int64_t exchange_bytes(const gspn_seq& s) { return counter_bytes(s) + flags_bytes(s) + words_bytes(s); }
+// What the workgroups tell each other: counters | flags | words.
+int64_t counter_bytes(const gspn_seq& s) { return (s.D + 63) / 64 * 64; }   // 64 for the narrowest block
+
+int64_t flags_bytes(const gspn_seq& s, int tile) {
+    return ((s.D + 63) / 64 * total_tiles(s, tile) * 4 + 15) / 16 * 16;
+}
+
+int64_t words_bytes(const gspn_seq& s, int tile) {
+    return (int64_t)total_tiles(s, tile) * ((s.D + 127) / 128 * 128) * 8;
+}
+
+int64_t exchange_bytes(const gspn_seq& s, int tile) {
+    return tiles_wait(s, tile) ? counter_bytes(s) + flags_bytes(s, tile) + words_bytes(s, tile) : 0;
+}
 
 int power_of_two_in(int64_t v, int most) {
     int p = 1;
@@ -717,105 +753,91 @@ int power_of_two_in(int64_t v, int most) {
     return p;
 }
 
-bool even(const void* p, int64_t stride) { return ((uintptr_t)p & 3) == 0 && stride % 2 == 0; }
+bool even(const void* p, int64_t stride) { return ((uintptr_t)p & 3) == 0 && (!p || stride % 2 == 0); }
 
 // Two channels a lane: bf16 rows whose pairs are whole 4-byte words, and no
 // pair with two gates of a shared kind.
 bool pairs(const gspn_seq& s) {
     return s.dtype == GSPN_BF16 && s.D % 2 == 0 && (s.ch_per_weight == 1 || s.ch_per_weight % 2 == 0) &&
-           even(s.x, s.x_stride) && even(s.lam, s.lam ? s.lam_stride : 0) && even(s.u, s.u ? s.u_stride : 0) &&
+           even(s.x, s.x_stride) && even(s.lam, s.lam_stride) && even(s.u, s.u_stride) &&
            (s.ch_per_weight > 1 || even(s.gate, s.gate_stride));
 }
 
-Launch plan(const gspn_seq& s, int V) {
+// The launch, with what the workgroups tell each other cleared.
+Launch plan(const gspn_seq& s, int V, int tile, hipStream_t stream) {
     Launch la;
     la.blocks = (uint32_t)((s.D + 64 * V - 1) / (64 * V));
-    la.tiles = s.offsets ? 0 : tiles_of_sequence<kSeqTile>(s.T, s.N);
-    la.total = total_tiles<kSeqTile>(s.offsets, s.T, s.N);
+    la.tiles = s.offsets ? 0 : tiles_of_sequence(s, tile);
+    la.total = total_tiles(s, tile);
     la.counters = nullptr;
     la.flags = nullptr;
     la.words = nullptr;
-    if (tiles_wait(s)) {
+    la.spacing = spacing_of(s.T, s.N);
+    if (tiles_wait(s, tile)) {
         la.counters = static_cast<uint32_t*>(s.work);
         la.flags = la.counters + counter_bytes(s) / 4;
-        la.words = reinterpret_cast<uint64_t*>(la.flags + flags_bytes(s) / 4);
+        la.words = reinterpret_cast<uint64_t*>(la.flags + flags_bytes(s, tile) / 4);
+        const int64_t nc = (counter_bytes(s) + flags_bytes(s, tile)) / 16, nw = words_bytes(s, tile) / 16;
+        const unsigned grid = (unsigned)std::min<int64_t>((nc + nw + 255) / 256, 2048);
+        hipLaunchKernelGGL(seq_clear_kernel, dim3(grid), dim3(256), 0, stream, reinterpret_cast<uint4*>(la.counters),
+                           nc, reinterpret_cast<uint4*>(la.words), nw);
     }
     return la;
 }
 
-void clear(const gspn_seq& s, const Launch& la, hipStream_t stream) {
-    if (!la.counters) return;
-    const int64_t nc = (counter_bytes(s) + flags_bytes(s)) / 16, nw = words_bytes(s) / 16;
-    const unsigned grid = (unsigned)std::min<int64_t>((nc + nw + 255) / 256, 2048);
-    hipLaunchKernelGGL(seq_clear_kernel, dim3(grid), dim3(256), 0, stream, reinterpret_cast<uint4*>(la.counters), nc,
-                       reinterpret_cast<uint4*>(la.words), nw);
-}
-
 // f(kernel) for the variant that the flags name.
-template <typename T, int V, typename F>
-void fwd_variant(bool shared, bool lam, bool u, F f) {
-    if (shared) {
-        if (lam) u ? f(seq_fwd_kernel<T, V, true, true, true>) : f(seq_fwd_kernel<T, V, true, true, false>);
-        else u ? f(seq_fwd_kernel<T, V, true, false, true>) : f(seq_fwd_kernel<T, V, true, false, false>);
+template <typename T, int V, int TOKENS, int WAVES, typename F>
+void fwd_variant(const gspn_seq& s, F f) {
+    const bool lam = s.lam != nullptr, u = s.u != nullptr;
+    if (s.ch_per_weight > 1) {
+        if (lam) u ? f(seq_fwd_kernel<T, V, true, true, true, TOKENS, WAVES>) : f(seq_fwd_kernel<T, V, true, true, false, TOKENS, WAVES>);
+        else u ? f(seq_fwd_kernel<T, V, true, false, true, TOKENS, WAVES>) : f(seq_fwd_kernel<T, V, true, false, false, TOKENS, WAVES>);
     } else {
-        if (lam) u ? f(seq_fwd_kernel<T, V, false, true, true>) : f(seq_fwd_kernel<T, V, false, true, false>);
-        else u ? f(seq_fwd_kernel<T, V, false, false, true>) : f(seq_fwd_kernel<T, V, false, false, false>);
+        if (lam) u ? f(seq_fwd_kernel<T, V, false, true, true, TOKENS, WAVES>) : f(seq_fwd_kernel<T, V, false, true, false, TOKENS, WAVES>);
+        else u ? f(seq_fwd_kernel<T, V, false, false, true, TOKENS, WAVES>) : f(seq_fwd_kernel<T, V, false, false, false, TOKENS, WAVES>);
     }
 }
 
-template <typename T, int V, typename F>
-void bwd_variant(bool shared, bool lam, bool u, F f) {
-    if (shared) {
-        if (lam) u ? f(seq_bwd_kernel<T, V, true, true, true>) : f(seq_bwd_kernel<T, V, true, true, false>);
-        else u ? f(seq_bwd_kernel<T, V, true, false, true>) : f(seq_bwd_kernel<T, V, true, false, false>);
+template <typename T, int V, int TOKENS, int WAVES, typename F>
+void bwd_variant(const gspn_seq& s, F f) {
+    const bool lam = s.lam != nullptr, u = s.u != nullptr;
+    if (s.ch_per_weight > 1) {
+        if (lam) u ? f(seq_bwd_kernel<T, V, true, true, true, TOKENS, WAVES>) : f(seq_bwd_kernel<T, V, true, true, false, TOKENS, WAVES>);
+        else u ? f(seq_bwd_kernel<T, V, true, false, true, TOKENS, WAVES>) : f(seq_bwd_kernel<T, V, true, false, false, TOKENS, WAVES>);
     } else {
-        if (lam) u ? f(seq_bwd_kernel<T, V, false, true, true>) : f(seq_bwd_kernel<T, V, false, true, false>);
-        else u ? f(seq_bwd_kernel<T, V, false, false, true>) : f(seq_bwd_kernel<T, V, false, false, false>);
+        if (lam) u ? f(seq_bwd_kernel<T, V, false, true, true, TOKENS, WAVES>) : f(seq_bwd_kernel<T, V, false, true, false, TOKENS, WAVES>);
+        else u ? f(seq_bwd_kernel<T, V, false, false, true, TOKENS, WAVES>) : f(seq_bwd_kernel<T, V, false, false, false, TOKENS, WAVES>);
     }
 }
 
-}  // namespace
-
-int64_t seq_workspace(const gspn_seq& s, bool backward) {
-    int64_t bytes = tiles_wait(s) ? exchange_bytes(s) : 0;
-    const int group = power_of_two_in(s.ch_per_weight, 64);   // the smallest that a launch may take
-    if (backward && group < s.ch_per_weight) bytes += s.T * (s.D / group) * 4;
-    return bytes;
-}
-
-hipError_t launch_seq_fwd(const gspn_seq& s, hipStream_t stream) {
+template <int TOKENS, int WAVES>
+void fwd_launch(const gspn_seq& s, hipStream_t stream) {
     const int V = pairs(s) && even(s.y, s.y_stride) ? 2 : 1;
-    const Launch la = plan(s, V);
-    clear(s, la, stream);
+    const Launch la = plan(s, V, TOKENS * WAVES, stream);
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(la.total * la.blocks), dim3(kWaves * 64), 0, stream, s, la);
+        hipLaunchKernelGGL(kernel, dim3(la.total * la.blocks), dim3(WAVES * 64), 0, stream, s, la);
     };
-    const bool shared = s.ch_per_weight > 1;
-    if (s.dtype == GSPN_F32) fwd_variant<float, 1>(shared, s.lam, s.u, go);
-    else if (V == 2) fwd_variant<uint16_t, 2>(shared, s.lam, s.u, go);
-    else fwd_variant<uint16_t, 1>(shared, s.lam, s.u, go);
-    return hipGetLastError();
+    if (s.dtype == GSPN_F32) fwd_variant<float, 1, TOKENS, WAVES>(s, go);
+    else if (V == 2) fwd_variant<uint16_t, 2, TOKENS, WAVES>(s, go);
+    else fwd_variant<uint16_t, 1, TOKENS, WAVES>(s, go);
 }
 
-hipError_t launch_seq_bwd(const gspn_seq& s, const gspn_seq_grad& g, hipStream_t stream) {
-    const int V = pairs(s) && even(g.gy, g.gy ? g.gy_stride : 0) && even(g.gx, g.gx ? g.gx_stride : 0) &&
-                          even(g.glam, g.glam ? g.glam_stride : 0) && even(g.gu, g.gu ? g.gu_stride : 0) &&
-                          (s.ch_per_weight > 1 || even(g.ggate, g.ggate ? g.ggate_stride : 0))
+template <int TOKENS, int WAVES>
+void bwd_launch(const gspn_seq& s, const gspn_seq_grad& g, hipStream_t stream) {
+    const int V = pairs(s) && even(g.gy, g.gy_stride) && even(g.gx, g.gx_stride) && even(g.glam, g.glam_stride) &&
+                          even(g.gu, g.gu_stride) && (s.ch_per_weight > 1 || even(g.ggate, g.ggate_stride))
                       ? 2 : 1;
-    const Launch la = plan(s, V);
+    const Launch la = plan(s, V, TOKENS * WAVES, stream);
     const int group = power_of_two_in(s.ch_per_weight, 64 * V);
     float* partial = nullptr;
     if (group < s.ch_per_weight && g.ggate)
-        partial = reinterpret_cast<float*>(static_cast<char*>(s.work) +
-                                           (la.counters ? exchange_bytes(s) : 0));
-    clear(s, la, stream);
+        partial = reinterpret_cast<float*>(static_cast<char*>(s.work) + exchange_bytes(s, TOKENS * WAVES));
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(la.total * la.blocks), dim3(kWaves * 64), 0, stream, s, g, la, group, partial);
+        hipLaunchKernelGGL(kernel, dim3(la.total * la.blocks), dim3(WAVES * 64), 0, stream, s, g, la, group, partial);
     };
-    const bool shared = s.ch_per_weight > 1;
-    if (s.dtype == GSPN_F32) bwd_variant<float, 1>(shared, s.lam, s.u, go);
-    else if (V == 2) bwd_variant<uint16_t, 2>(shared, s.lam, s.u, go);
-    else bwd_variant<uint16_t, 1>(shared, s.lam, s.u, go);
+    if (s.dtype == GSPN_F32) bwd_variant<float, 1, TOKENS, WAVES>(s, go);
+    else if (V == 2) bwd_variant<uint16_t, 2, TOKENS, WAVES>(s, go);
+    else bwd_variant<uint16_t, 1, TOKENS, WAVES>(s, go);
     if (partial && s.T) {
         const dim3 grid((unsigned)((s.T * (s.D / s.ch_per_weight) + 255) / 256));
         if (s.dtype == GSPN_BF16)
@@ -823,6 +845,30 @@ hipError_t launch_seq_bwd(const gspn_seq& s, const gspn_seq_grad& g, hipStream_t
         else
             hipLaunchKernelGGL(reduce_gate_kernel<float>, grid, dim3(256), 0, stream, s, g, group, partial);
     }
+}
+
+}  // namespace
+
+int64_t seq_states_rows(int64_t T, int64_t N) { return T / spacing_of(T, N) + N; }
+
+int64_t seq_tiles(int64_t T, int64_t N) { return T / spacing_of(T, N) + N + 1; }
+
+int64_t seq_workspace(const gspn_seq& s, bool backward) {
+    int64_t bytes = exchange_bytes(s, tile_of(s, backward));
+    const int group = power_of_two_in(s.ch_per_weight, 64);   // the smallest that a launch may take
+    if (backward && group < s.ch_per_weight) bytes += s.T * (s.D / group) * 4;
+    return bytes;
+}
+
+hipError_t launch_seq_fwd(const gspn_seq& s, hipStream_t stream) {
+    if (short_sequences(s)) fwd_launch<8, 4>(s, stream);
+    else fwd_launch<32, 8>(s, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_seq_bwd(const gspn_seq& s, const gspn_seq_grad& g, hipStream_t stream) {
+    if (short_sequences(s)) bwd_launch<8, 4>(s, g, stream);
+    else bwd_launch<16, 8>(s, g, stream);
     return hipGetLastError();
 }
 

@@ -19,9 +19,11 @@ they were in an ``out`` of the caller's.
 """
 from __future__ import annotations
 
-import ctypes
-
 from . import _lib
+
+_PACK_SEQ = _lib.packer(_lib.Seq)
+_PACK_GRAD = _lib.packer(_lib.SeqGrad)
+_PACK_TOKEN = _lib.packer(_lib.SeqToken)
 
 
 def _code(t):
@@ -36,7 +38,7 @@ def _code(t):
 def _row_stride(name, t):
     """Elements from one row to the next of a [rows, width] or [B, L, width] tensor."""
     shape, stride = t.shape, t.stride()
-    if shape[-1] > 1 and stride[-1] != 1:
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     if len(shape) == 2:
         return stride[0] if shape[0] > 1 else shape[1]
@@ -51,7 +53,9 @@ def _row_stride(name, t):
 
 
 def _like(name, t, x, shape):
-    """t's pointer and row stride; checks device, dtype and shape against x's."""
+    """t's pointer and row stride, (0, 0) for None; checks device, dtype and shape against x's."""
+    if t is None:
+        return 0, 0
     if t.device != x.device:
         raise ValueError(f"{name} is on {t.device}, x is on {x.device}")
     if t.dtype != x.dtype:
@@ -63,6 +67,8 @@ def _like(name, t, x, shape):
 
 def _states(name, t, dev, shape):
     import torch
+    if t is None:
+        return 0
     if t.device != dev or t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 {tuple(shape)} tensor on {dev}")
     return t.data_ptr()
@@ -70,6 +76,8 @@ def _states(name, t, dev, shape):
 
 def _index(name, t, dev):
     import torch
+    if t is None:
+        return 0
     if t.device != dev or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous one-dimensional int32 tensor on {dev}")
     return t.data_ptr()
@@ -77,76 +85,62 @@ def _index(name, t, dev):
 
 def _layout(x, offsets):
     """(T, N) of a packed or an equal-rows tensor."""
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("tensors must be on a GPU (HIP) device")
-    if x.dim() == 3:
+    shape = x.shape
+    if len(shape) == 3:
         if offsets is not None:
             raise ValueError("offsets go with packed [T, D] tensors; [B, L, D] has rows of equal length")
-        if x.shape[0] == 0:
+        if shape[0] == 0:
             raise ValueError("there must be a sequence")
-        return x.shape[0] * x.shape[1], x.shape[0]
-    if x.dim() != 2:
+        return shape[0] * shape[1], shape[0]
+    if len(shape) != 2:
         raise ValueError("x must be [T, D] or [B, L, D]")
     if offsets is None:
-        return x.shape[0], 1
+        return shape[0], 1
     if offsets.numel() < 2:
         raise ValueError("offsets must hold N + 1 numbers, N >= 1")
-    return x.shape[0], offsets.numel() - 1
+    return shape[0], offsets.numel() - 1
 
 
 def _call(fn, dev, *args):
     """fn(*args, the current stream of dev), with dev current."""
     import torch
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, stream)
+    index = dev.index
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream)
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc:
         _lib.check(rc)
 
 
-def _sequence(x, gate, lam, u, offsets, h0, ch_per_weight):
-    """The gspn_seq of the inputs (outputs and workspace are the caller's to fill in)."""
+def _sizes(x, ch_per_weight, offsets):
+    """(T, N, D) of a call."""
     T, N = _layout(x, offsets)
     D = x.shape[-1]
     if ch_per_weight < 1 or D % ch_per_weight:
         raise ValueError("ch_per_weight must divide D")
-    s = _lib.Seq(T=T, D=D, N=N, ch_per_weight=ch_per_weight, dtype=_code(x))
-    s.x, s.x_stride = x.data_ptr(), _row_stride("x", x)
-    s.gate, s.gate_stride = _like("gate", gate, x, x.shape[:-1] + (D // ch_per_weight,))
-    if lam is not None:
-        s.lam, s.lam_stride = _like("lam", lam, x, x.shape)
-    if u is not None:
-        s.u, s.u_stride = _like("u", u, x, x.shape)
-    if offsets is not None:
-        s.offsets = _index("offsets", offsets, x.device)
-    if h0 is not None:
-        s.h0 = _states("h0", h0, x.device, (N, D))
-    return s
+    return T, N, D
 
 
-def _workspace(s, dev, backward):
-    """Allocates the workspace that s asks for; the tensor has to live until the call is enqueued."""
+def _gate(gate, x, D, ch_per_weight):
+    return _like("gate", gate, x, x.shape if ch_per_weight == 1 else x.shape[:-1] + (D // ch_per_weight,))
+
+
+def _workspace(kept, T, D, N, offsets, ch_per_weight, code, backward, dev):
+    """(pointer, bytes) of a new workspace, which `kept` (a list) keeps until the call is enqueued."""
     import torch
-    need = _lib.load().gspn_seq_workspace(ctypes.byref(s), backward)
+    need = _lib.load().gspn_seq_workspace(
+        _PACK_SEQ(0, 0, 0, 0, offsets, 0, 0, 0, 0, 0, 0, T, D, N, 0, 0, 0, 0, 0, ch_per_weight, code, 0), backward)
     if need < 0:
         _lib.check(need)
     if need == 0:
-        return None
+        return 0, 0
     work = torch.empty(need, dtype=torch.uint8, device=dev)
-    s.work, s.work_bytes = work.data_ptr(), need
-    return work
-
-
-def _output(name, out, like, shape, s):
-    """An output tensor: the caller's, checked, or a new one whose rows behind the last sequence are to be zero."""
-    import torch
-    if out is None:
-        s.flags = _lib.SEQ_ZERO_TAIL
-        out = torch.empty(shape, dtype=like.dtype, device=like.device)
-    return (out,) + _like(name, out, like, shape)
+    kept.append(work)
+    return work.data_ptr(), need
 
 
 def seq_scan_fwd(x, gate, *, lam=None, u=None, offsets=None, h0=None, ch_per_weight: int = 1, out=None,
@@ -155,20 +149,31 @@ def seq_scan_fwd(x, gate, *, lam=None, u=None, offsets=None, h0=None, ch_per_wei
 
     y is shaped like x; h_last [N, D] float32 is each sequence's state behind
     its last token (h0's for a sequence of none).  return_states adds what
-    seq_scan_bwd needs: the state in front of every 128th token of a sequence.
+    seq_scan_bwd starts from: states inside the sequences, float32, some tokens apart.
     """
     import torch
-    s = _sequence(x, gate, lam, u, offsets, h0, ch_per_weight)
-    y, s.y, s.y_stride = _output("out", out, x, x.shape, s)
-    h_last = torch.empty((s.N, s.D), dtype=torch.float32, device=x.device)
-    s.h_last = h_last.data_ptr()
-    states = None
+    T, N, D = _sizes(x, ch_per_weight, offsets)
+    dev, code, shape, kept = x.device, _code(x), x.shape, []
+    px, sx = x.data_ptr(), _row_stride("x", x)
+    pg, sg = _gate(gate, x, D, ch_per_weight)
+    pl, sl = _like("lam", lam, x, shape)
+    pu, su = _like("u", u, x, shape)
+    po = _index("offsets", offsets, dev)
+    ph = _states("h0", h0, dev, (N, D))
+    # rows behind the last sequence are zero in a new tensor
+    flags = 0 if out is not None or offsets is None else _lib.SEQ_ZERO_TAIL
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
+    py, sy = _like("out", out, x, shape)
+    h_last = torch.empty((N, D), dtype=torch.float32, device=dev)
+    lib, states, ps = _lib.load(), None, 0
     if return_states:
-        states = torch.empty((_lib.load().gspn_seq_states_rows(s.T, s.N), s.D), dtype=torch.float32, device=x.device)
-        s.states = states.data_ptr()
-    work = _workspace(s, x.device, 0)   # noqa: F841 -- lives until the call is enqueued
-    _call(_lib.load().gspn_seq_fwd, x.device, ctypes.byref(s))
-    return (y, h_last, states) if return_states else (y, h_last)
+        states = torch.empty((lib.gspn_seq_states_rows(T, N), D), dtype=torch.float32, device=dev)
+        ps = states.data_ptr()
+    pw, nw = _workspace(kept, T, D, N, po, ch_per_weight, code, 0, dev)
+    _call(lib.gspn_seq_fwd, dev, _PACK_SEQ(px, pg, pl, pu, po, ph, py, h_last.data_ptr(), ps, pw, nw, T, D, N, sx, sg,
+                                           sl, su, sy, ch_per_weight, code, flags))
+    return (out, h_last, states) if return_states else (out, h_last)
 
 
 def seq_scan_bwd(x, gate, gy, states, *, lam=None, u=None, offsets=None, gh_last=None, ch_per_weight: int = 1,
@@ -182,39 +187,42 @@ def seq_scan_bwd(x, gate, gy, states, *, lam=None, u=None, offsets=None, gh_last
     belongs to h0, whether or not the forward had one.  ``out`` may give the
     five tensors.
     """
+    if out is not None:
+        if len(out) != 5 or any((o is None) != (t is None) for o, t in zip(out, (x, gate, lam, u, x))):
+            raise ValueError("out must hold a tensor for every gradient: gx, ggate, gh0, and glam and gu with lam and u "
+                             "(None without)")
     return _backward(x, gate, gy, states, lam, u, offsets, gh_last, ch_per_weight, out, (True,) * 5)
 
 
 def _backward(x, gate, gy, states, lam, u, offsets, gh_last, ch_per_weight, out, want):
     import torch
-    s = _sequence(x, gate, lam, u, offsets, None, ch_per_weight)
-    g = _lib.SeqGrad()
-    lib = _lib.load()
-    s.states = _states("states", states, x.device, (lib.gspn_seq_states_rows(s.T, s.N), s.D))
-    if gy is not None:
-        g.gy, g.gy_stride = _like("gy", gy, x, x.shape)
-    if gh_last is not None:
-        g.gh_last = _states("gh_last", gh_last, x.device, (s.N, s.D))
-    given = (None,) * 5 if out is None else out
-    if len(given) != 5:
-        raise ValueError("out must hold five tensors: gx, ggate, glam, gu, gh0")
-    if out is not None and any((o is None) != (t is None) for o, t in zip(out, (x, gate, lam, u, x))):
-        raise ValueError("out must hold a tensor for every gradient: gx, ggate, gh0, and glam and gu with lam and u")
-    grads = [None] * 5
-    if want[0]:
-        grads[0], g.gx, g.gx_stride = _output("gx", given[0], x, x.shape, s)
-    if want[1]:
-        grads[1], g.ggate, g.ggate_stride = _output("ggate", given[1], x, gate.shape, s)
-    if want[2] and lam is not None:
-        grads[2], g.glam, g.glam_stride = _output("glam", given[2], x, x.shape, s)
-    if want[3] and u is not None:
-        grads[3], g.gu, g.gu_stride = _output("gu", given[3], x, x.shape, s)
-    if want[4]:
-        grads[4] = given[4] if given[4] is not None else torch.empty((s.N, s.D), dtype=torch.float32, device=x.device)
-        g.gh0 = _states("gh0", grads[4], x.device, (s.N, s.D))
-    work = _workspace(s, x.device, 1)   # noqa: F841 -- lives until the call is enqueued
-    _call(lib.gspn_seq_bwd, x.device, ctypes.byref(s), ctypes.byref(g))
-    return tuple(grads)
+    T, N, D = _sizes(x, ch_per_weight, offsets)
+    dev, code, shape, kept, lib = x.device, _code(x), x.shape, [], _lib.load()
+    px, sx = x.data_ptr(), _row_stride("x", x)
+    pg, sg = _gate(gate, x, D, ch_per_weight)
+    pl, sl = _like("lam", lam, x, shape)
+    pu, su = _like("u", u, x, shape)
+    po = _index("offsets", offsets, dev)
+    if states is None:
+        raise ValueError("states must be what seq_scan_fwd returned")
+    ps = _states("states", states, dev, (lib.gspn_seq_states_rows(T, N), D))
+    py, sy = _like("gy", gy, x, shape)
+    ph = _states("gh_last", gh_last, dev, (N, D))
+    flags = 0 if out is not None or offsets is None else _lib.SEQ_ZERO_TAIL
+    if out is None:
+        new = [None if t is None or not w else torch.empty(t.shape, dtype=x.dtype, device=dev)
+               for t, w in zip((x, gate, lam, u), want)]
+        out = new + [torch.empty((N, D), dtype=torch.float32, device=dev) if want[4] else None]
+    gx, tx = _like("gx", out[0], x, shape)
+    gg, tg = _like("ggate", out[1], x, gate.shape)
+    gl, tl = _like("glam", out[2], x, shape)
+    gu, tu = _like("gu", out[3], x, shape)
+    gh = _states("gh0", out[4], dev, (N, D))
+    pw, nw = _workspace(kept, T, D, N, po, ch_per_weight, code, 1, dev)
+    _call(lib.gspn_seq_bwd, dev,
+          _PACK_SEQ(px, pg, pl, pu, po, 0, 0, 0, ps, pw, nw, T, D, N, sx, sg, sl, su, 0, ch_per_weight, code, flags),
+          _PACK_GRAD(py, ph, gx, gg, gl, gu, gh, sy, tx, tg, tl, tu))
+    return tuple(out)
 
 
 def _autograd_function():
@@ -284,29 +292,28 @@ def seq_step(x, gate, state, *, lam=None, u=None, slots=None, ch_per_weight: int
     request and are taken in order.
     """
     import torch
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("tensors must be on a GPU (HIP) device")
-    if x.dim() != 2 or state.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2 or state.dim() != 2:
         raise ValueError("x must be [N, D] and state [S, D]")
-    N, D = x.shape
+    N, D = shape
     if ch_per_weight < 1 or D % ch_per_weight:
         raise ValueError("ch_per_weight must divide D")
-    S = state.shape[0]
-    t = _lib.SeqToken(N=N, S=S, D=D, ch_per_weight=ch_per_weight, dtype=_code(x))
-    t.x, t.x_stride = x.data_ptr(), _row_stride("x", x)
-    t.gate, t.gate_stride = _like("gate", gate, x, (N, D // ch_per_weight))
-    if lam is not None:
-        t.lam, t.lam_stride = _like("lam", lam, x, x.shape)
-    if u is not None:
-        t.u, t.u_stride = _like("u", u, x, x.shape)
-    t.state = _states("state", state, x.device, (S, D))
-    if slots is not None:
-        if slots.shape != (N,):
-            raise ValueError(f"slots must hold {N} numbers")
-        t.slots = _index("slots", slots, x.device)
+    dev, code, S = x.device, _code(x), state.shape[0]
+    sx = _row_stride("x", x)
+    pg, sg = _gate(gate, x, D, ch_per_weight)
+    pl, sl = _like("lam", lam, x, shape)
+    pu, su = _like("u", u, x, shape)
+    pt = _states("state", state, dev, (S, D))
+    if slots is not None and slots.shape != (N,):
+        raise ValueError(f"slots must hold {N} numbers")
+    pi = _index("slots", slots, dev)
+    flags = 0
     if out is None:
-        # rows of padding are not written by the kernel
-        out = (torch.empty if slots is None else torch.zeros)((N, D), dtype=x.dtype, device=x.device)
-    t.y, t.y_stride = _like("out", out, x, x.shape)
-    _call(_lib.load().gspn_seq_step, x.device, ctypes.byref(t))
+        flags = _lib.SEQ_ZERO_TAIL
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
+    py, sy = _like("out", out, x, shape)
+    _call(_lib.load().gspn_seq_step, dev, _PACK_TOKEN(x.data_ptr(), pg, pl, pu, pi, pt, py, N, S, D, sx, sg, sl, su, sy,
+                                                      ch_per_weight, code, flags))
     return out

@@ -35,6 +35,32 @@ def test_forward_lengths(dtype, lens, D, cpw):
     check(c, call(c))
 
 
+# many tiles behind one another: one sequence, one among single tokens, equal rows
+LONG = [[5003], [1] * 150 + [3001], [2, 0, 2500, 1000, 1]]
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 8), ("bf16", 134)])
+@pytest.mark.parametrize("lens", LONG, ids=lambda v: f"{len(v)}seq{sum(v)}")
+def test_long_sequences(dtype, D, lens):
+    say(f"long {dtype} {len(lens)} sequences, {sum(lens)} tokens, D {D}")
+    c = make(lens, D, dtype=dtype, cpw=2, pad=2, seed=sum(lens))
+    check(c, call(c))
+    check_grads(c, grads(c))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L", [(2, 1800), (70, 40)])
+def test_many_equal_rows(dtype, B, L):
+    import linear_spatial_propagation_amd as gspn
+    say(f"equal rows {dtype} {B} x {L}, both directions")
+    c = make([L] * B, 40, dtype=dtype, cpw=8, lam=False, seed=B)
+    x, gate, u, gy = (up(c[k]).view(B, L, -1) for k in ("x", "gate", "u", "gy"))
+    y, last, st = gspn.seq_scan_fwd(x, gate, u=u, h0=up(c["h0"]), ch_per_weight=8, return_states=True)
+    check(c, (y.view(B * L, 40), last))
+    g = gspn.seq_scan_bwd(x, gate, gy, st, u=u, gh_last=up(c["gh"]), ch_per_weight=8)
+    check_grads(c, [None if t is None else t.reshape(-1, t.shape[-1]) for t in g])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("D,cpw", WIDTHS)
 @pytest.mark.parametrize("lam,u,h0", [(True, True, True), (False, False, False), (True, False, False), (False, True, True)])

@@ -83,14 +83,14 @@ def test_null_structs(lib):
 
 def token(**kw):
     v = dict(x=at(0), gate=at(1), lam=at(2), u=at(3), slots=at(4), state=at(5), y=at(6), N=8, S=16, D=64, x_stride=64,
-             gate_stride=64, lam_stride=64, u_stride=64, y_stride=64, ch_per_weight=1, dtype=0)
+             gate_stride=64, lam_stride=64, u_stride=64, y_stride=64, ch_per_weight=1, dtype=0, flags=0)
     v.update(kw)
     return _lib.SeqToken(**v)
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(N=-1), SHAPE), (dict(S=0), SHAPE), (dict(D=0), SHAPE), (dict(slots=0, N=17), SHAPE), (dict(N=1 << 21), SHAPE),
-    (dict(ch_per_weight=5), CPW), (dict(dtype=9), DTYPE), (dict(state=0), NULL), (dict(x=0), NULL), (dict(y=0), NULL),
+    (dict(ch_per_weight=5), CPW), (dict(dtype=9), DTYPE), (dict(flags=2), FLAGS), (dict(state=0), NULL), (dict(x=0), NULL), (dict(y=0), NULL),
     (dict(y_stride=1), STRIDE), (dict(u_stride=-4), STRIDE), (dict(x=at(0) + 2), ALIGN), (dict(state=at(5) + 1), ALIGN),
     (dict(y=at(0)), ALIAS), (dict(state=at(2)), ALIAS), (dict(y=at(5) + 4), ALIAS), (dict(state=at(4)), ALIAS),
 ], ids=str)
