@@ -432,7 +432,7 @@ typedef struct {
     const float *h0;            /* [N][D], may be NULL */
     void *y;                    /* [T][D] output (gspn_seq_bwd: not used) */
     float *h_last;              /* [N][D] output, may be NULL (gspn_seq_bwd: not used) */
-    float *states;              /* [gspn_seq_states_rows(T, N)][D]: gspn_seq_fwd writes what gspn_seq_bwd
+    float *states;              /* [gspn_seq_states_rows(T, N, offsets != NULL)][D]: gspn_seq_fwd writes what gspn_seq_bwd
                                    reads, NULL to write none */
     void *work;                 /* gspn_seq_workspace bytes, NULL where that is 0 */
     int64_t work_bytes;
@@ -474,8 +474,9 @@ int gspn_seq_bwd(const gspn_seq *seq, const gspn_seq_grad *grad, hipStream_t str
  * pointers are not used.  A negative code for invalid sizes. */
 int64_t gspn_seq_workspace(const gspn_seq *seq, int32_t backward);
 
-/* Rows of `states`, or a negative code for invalid sizes. */
-int64_t gspn_seq_states_rows(int64_t T, int64_t N);
+/* Rows of `states` for packed rows (offsets given) or rows of equal length
+ * (packed = 0), or a negative code for invalid sizes. */
+int64_t gspn_seq_states_rows(int64_t T, int64_t N, int32_t packed);
 
 /*
  * One token for each of N requests, whose states live in a cache:

@@ -139,7 +139,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.gspn_seq_bwd.argtypes = [vp, vp, vp]
         lib.gspn_seq_step.argtypes = [vp, vp]
         lib.gspn_seq_workspace.argtypes = [vp, i32]
-        lib.gspn_seq_states_rows.argtypes = [i64, i64]
+        lib.gspn_seq_states_rows.argtypes = [i64, i64, i32]
         lib.gspn_adapter_add.argtypes = [vp, vp]
         lib.gspn_adapter_workspace.argtypes = [vp]
         for name in ("gspn_seq_fwd", "gspn_seq_bwd", "gspn_seq_step", "gspn_adapter_add"):

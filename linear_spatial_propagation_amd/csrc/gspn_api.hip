@@ -610,7 +610,7 @@ int check_seq_sizes(int64_t T, int64_t D, int64_t N, int32_t cpw, int32_t dtype,
     if (check_dtype(dtype)) return GSPN_ERR_DTYPE;
     // 32-bit launches: at most one workgroup of 512 threads for a tile of
     // tokens, or a sequence's rest, and 64 channels
-    if (gspn::seq_tiles(T, N) * ((D + 63) / 64) > (1LL << 22)) return GSPN_ERR_SHAPE;
+    if ((gspn::seq_states_rows(T, N, packed) + 1) * ((D + 63) / 64) > (1LL << 22)) return GSPN_ERR_SHAPE;
     return GSPN_OK;
 }
 
@@ -636,9 +636,9 @@ bool rows_overlap(const void* p, int64_t rows, int64_t stride, int64_t width) {
 
 extern "C" {
 
-int64_t gspn_seq_states_rows(int64_t T, int64_t N) {
-    if (T < 0 || N < 1 || T > kMaxTokens || N > kMaxTokens) return GSPN_ERR_SHAPE;
-    return gspn::seq_states_rows(T, N);
+int64_t gspn_seq_states_rows(int64_t T, int64_t N, int32_t packed) {
+    if (T < 0 || N < 1 || T > kMaxTokens || N > kMaxTokens || (!packed && T % N)) return GSPN_ERR_SHAPE;
+    return gspn::seq_states_rows(T, N, packed != 0);
 }
 
 int64_t gspn_seq_workspace(const gspn_seq* seq, int32_t backward) {
@@ -666,7 +666,7 @@ int gspn_seq_fwd(const gspn_seq* seq, hipStream_t stream) {
     const int64_t need = gspn::seq_workspace(s, false);
     const Span outs[] = {{s.y, rows_bytes(s.T, s.y_stride, s.D, es)},
                          {s.h_last, state},
-                         {s.states, (size_t)gspn_seq_states_rows(s.T, s.N) * s.D * 4},
+                         {s.states, (size_t)gspn::seq_states_rows(s.T, s.N, s.offsets != nullptr) * s.D * 4},
                          {s.work, (size_t)need}};
     if (check_apart(outs, 4, ins, 6)) return GSPN_ERR_ALIAS;
     if (need > 0 && (!s.work || s.work_bytes < need)) return GSPN_ERR_WORK;
@@ -698,7 +698,7 @@ int gspn_seq_bwd(const gspn_seq* seq, const gspn_seq_grad* grad, hipStream_t str
                         {s.lam, rows_bytes(s.T, s.lam_stride, s.D, es)},
                         {s.u, rows_bytes(s.T, s.u_stride, s.D, es)},
                         {s.offsets, ((size_t)s.N + 1) * 4},
-                        {s.states, (size_t)gspn_seq_states_rows(s.T, s.N) * s.D * 4},
+                        {s.states, (size_t)gspn::seq_states_rows(s.T, s.N, s.offsets != nullptr) * s.D * 4},
                         {g.gy, rows_bytes(s.T, g.gy_stride, s.D, es)},
                         {g.gh_last, state}};
     const int64_t need = gspn::seq_workspace(s, true);

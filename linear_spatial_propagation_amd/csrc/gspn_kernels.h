@@ -92,8 +92,7 @@ hipError_t launch_general(const ScanArgs& a, float* planes, hipStream_t stream);
 
 // Sequences (gspn_seq.hip).  The arguments are validated; sizes as the C ABI
 // has them.  seq_workspace: bytes, for the forward or the backward.
-int64_t seq_states_rows(int64_t T, int64_t N);   // rows of gspn_seq.states
-int64_t seq_tiles(int64_t T, int64_t N);         // most workgroups of a launch for a block of 64 channels
+int64_t seq_states_rows(int64_t T, int64_t N, bool packed);   // rows of gspn_seq.states
 int64_t seq_workspace(const gspn_seq& s, bool backward);
 hipError_t launch_seq_fwd(const gspn_seq& s, hipStream_t stream);
 hipError_t launch_seq_bwd(const gspn_seq& s, const gspn_seq_grad& g, hipStream_t stream);

@@ -206,9 +206,23 @@ struct Launch {
     int spacing;            // tokens between two saved states
 };
 
-// Tokens between two saved states: of long sequences 128, of many short ones 32.
-// It goes by T and N alone, as `states` is sized before anything else is known.
-inline int spacing_of(int64_t T, int64_t N) { return T <= 32 * N ? 32 : 128; }
+// How a call's tiles are laid out.  It goes by T, N and the layout alone, as
+// `states` is sized before anything else is known.
+//   kShort: sequences of up to 32 tokens on average, which would leave most waves of
+//           larger tiles without one;
+//   kRows:  many rows of equal length: a tile seldom waits (tile_number), and small
+//           ones let more workgroups into a CU;
+//   kLong:  the rest: the fewer tiles there are in a row, the fewer wait.
+enum Kind { kShort, kRows, kLong };
+inline Kind kind_of(int64_t T, int64_t N, bool packed) {
+    return T <= 32 * N ? kShort : !packed && N >= 8 ? kRows : kLong;
+}
+
+// Tokens between two saved states; the backward's tile.
+inline int spacing_of(int64_t T, int64_t N, bool packed) {
+    const Kind kind = kind_of(T, N, packed);
+    return kind == kShort ? 32 : kind == kRows ? 64 : 128;
+}
 
 // The workgroup's tile: from the counter where tiles wait for each other.  Rows of
 // equal length are taken tile by tile across the sequences (the backward: from
@@ -713,13 +727,26 @@ __global__ __launch_bounds__(256) void seq_step_kernel(gspn_seq_token s) {
 }
 
 // ---------------------------------------------------------------- host
-// Forward tiles are 256 tokens (eight waves of 32): the fewer tiles, the fewer
-// wait for each other.  The backward holds more for a token and takes 128 (eight
-// of 16).  Many short sequences would leave most waves of such tiles without a
-// token: theirs are 32 (four waves of 8).
-bool short_sequences(const gspn_seq& s) { return spacing_of(s.T, s.N) == 32; }
+Kind kind_of(const gspn_seq& s) { return kind_of(s.T, s.N, s.offsets != nullptr); }
 
-int tile_of(const gspn_seq& s, bool backward) { return short_sequences(s) ? 32 : backward ? 128 : 256; }
+// Tokens of a forward tile (bf16, lam and u):
+//   512 sequences of 16 tokens, 2048 channels: 34 us with tiles of 32, 56 with 64;
+//   16 rows of 2048, 1152 channels, a gate for 8: 75 us with 64, 83 with 128, 92 with 256;
+//   40 sequences of 12001 tokens, 2048 channels: 49 us with 128 (two workgroups of
+//   it fit a CU), 56 with 256;
+//   one of 131072, 1024 channels, no lam or u: 220 us with 256, 271 with 128.
+int forward_tile(const gspn_seq& s) {
+    const Kind kind = kind_of(s);
+    if (kind != kLong) return spacing_of(s.T, s.N, s.offsets != nullptr);
+    return s.N * ((s.D + 127) / 128) >= 64 ? 128 : 256;
+}
+
+// The backward holds more for a token: at most 128 (the 16 rows: 122 us with
+// tiles of 64, 136 with 128; one row of 32768 tokens of 320 channels in fp32: 70
+// and 55 us).
+int tile_of(const gspn_seq& s, bool backward) {
+    return backward ? spacing_of(s.T, s.N, s.offsets != nullptr) : forward_tile(s);
+}
 
 uint32_t tiles_of_sequence(const gspn_seq& s, int tile) {
     const int64_t rows = s.T / s.N;
@@ -772,7 +799,7 @@ Launch plan(const gspn_seq& s, int V, int tile, hipStream_t stream) {
     la.counters = nullptr;
     la.flags = nullptr;
     la.words = nullptr;
-    la.spacing = spacing_of(s.T, s.N);
+    la.spacing = spacing_of(s.T, s.N, s.offsets != nullptr);
     if (tiles_wait(s, tile)) {
         la.counters = static_cast<uint32_t*>(s.work);
         la.flags = la.counters + counter_bytes(s) / 4;
@@ -849,9 +876,7 @@ void bwd_launch(const gspn_seq& s, const gspn_seq_grad& g, hipStream_t stream) {
 
 }  // namespace
 
-int64_t seq_states_rows(int64_t T, int64_t N) { return T / spacing_of(T, N) + N; }
-
-int64_t seq_tiles(int64_t T, int64_t N) { return T / spacing_of(T, N) + N + 1; }
+int64_t seq_states_rows(int64_t T, int64_t N, bool packed) { return T / spacing_of(T, N, packed) + N; }
 
 int64_t seq_workspace(const gspn_seq& s, bool backward) {
     int64_t bytes = exchange_bytes(s, tile_of(s, backward));
@@ -861,14 +886,21 @@ int64_t seq_workspace(const gspn_seq& s, bool backward) {
 }
 
 hipError_t launch_seq_fwd(const gspn_seq& s, hipStream_t stream) {
-    if (short_sequences(s)) fwd_launch<8, 4>(s, stream);
-    else fwd_launch<32, 8>(s, stream);
+    switch (forward_tile(s)) {
+        case 32: fwd_launch<8, 4>(s, stream); break;
+        case 64: fwd_launch<16, 4>(s, stream); break;
+        case 128: fwd_launch<32, 4>(s, stream); break;
+        default: fwd_launch<32, 8>(s, stream); break;
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_seq_bwd(const gspn_seq& s, const gspn_seq_grad& g, hipStream_t stream) {
-    if (short_sequences(s)) bwd_launch<8, 4>(s, g, stream);
-    else bwd_launch<16, 8>(s, g, stream);
+    switch (kind_of(s)) {
+        case kShort: bwd_launch<8, 4>(s, g, stream); break;
+        case kRows: bwd_launch<8, 8>(s, g, stream); break;
+        default: bwd_launch<16, 8>(s, g, stream); break;
+    }
     return hipGetLastError();
 }
 

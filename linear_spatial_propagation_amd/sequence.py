@@ -168,7 +168,7 @@ def seq_scan_fwd(x, gate, *, lam=None, u=None, offsets=None, h0=None, ch_per_wei
     h_last = torch.empty((N, D), dtype=torch.float32, device=dev)
     lib, states, ps = _lib.load(), None, 0
     if return_states:
-        states = torch.empty((lib.gspn_seq_states_rows(T, N), D), dtype=torch.float32, device=dev)
+        states = torch.empty((lib.gspn_seq_states_rows(T, N, po != 0), D), dtype=torch.float32, device=dev)
         ps = states.data_ptr()
     pw, nw = _workspace(kept, T, D, N, po, ch_per_weight, code, 0, dev)
     _call(lib.gspn_seq_fwd, dev, _PACK_SEQ(px, pg, pl, pu, po, ph, py, h_last.data_ptr(), ps, pw, nw, T, D, N, sx, sg,
@@ -205,7 +205,7 @@ def _backward(x, gate, gy, states, lam, u, offsets, gh_last, ch_per_weight, out,
     po = _index("offsets", offsets, dev)
     if states is None:
         raise ValueError("states must be what seq_scan_fwd returned")
-    ps = _states("states", states, dev, (lib.gspn_seq_states_rows(T, N), D))
+    ps = _states("states", states, dev, (lib.gspn_seq_states_rows(T, N, po != 0), D))
     py, sy = _like("gy", gy, x, shape)
     ph = _states("gh_last", gh_last, dev, (N, D))
     flags = 0 if out is not None or offsets is None else _lib.SEQ_ZERO_TAIL

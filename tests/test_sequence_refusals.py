@@ -124,9 +124,12 @@ def test_adapter_refuses(lib, kw, code):
 
 
 def test_sizes(lib):
-    assert lib.gspn_seq_states_rows(0, 3) == 3
-    assert lib.gspn_seq_states_rows(130, 2) == 3
-    assert lib.gspn_seq_states_rows(-1, 2) == SHAPE
+    for packed in (0, 1):
+        assert lib.gspn_seq_states_rows(0, 3, packed) == 3
+        assert lib.gspn_seq_states_rows(-2, 2, packed) == SHAPE
+        # a row for the start of each sequence, and for every so many tokens
+        assert 2 + 1000 // 256 <= lib.gspn_seq_states_rows(1000, 2, packed) <= 2 + 1000 // 32
+    assert lib.gspn_seq_states_rows(131, 2, 0) == SHAPE
     assert lib.gspn_seq_workspace(ctypes.byref(seq(N=0)), 0) == SHAPE
     assert lib.gspn_adapter_workspace(ctypes.byref(adapter(r=300))) == SHAPE
     assert lib.gspn_adapter_add(ctypes.byref(adapter(T=0, base=0, x=0, out=0)), None) == 0
