@@ -104,6 +104,27 @@ __device__ __forceinline__ Frag<float> load8(const float* __restrict__ p, int64_
     return f;
 }
 
+// p[0 .. 3] in the low half of a piece.
+__device__ __forceinline__ void load4(Frag<uint16_t>& f, int half, const uint16_t* __restrict__ p) {
+    const auto v = *reinterpret_cast<const Piece<uint16_t>::x2*>(p);
+    u32x4 w = __builtin_bit_cast(u32x4, f.v);
+    w[2 * half] = v.x, w[2 * half + 1] = v.y;
+    f.v = __builtin_bit_cast(bf16x8, w);
+}
+__device__ __forceinline__ void load4(Frag<float>& f, int half, const float* __restrict__ p) {
+    const f32x4 v = *reinterpret_cast<const Piece<float>::x4*>(p);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f.v[4 * half + e] = v[e];
+}
+__device__ __forceinline__ void keep4(uint16_t* p, const Frag<uint16_t>& f, int half) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x4 w = __builtin_bit_cast(u32x4, f.v);
+    *reinterpret_cast<u32x2*>(p) = u32x2{w[2 * half], w[2 * half + 1]};
+}
+__device__ __forceinline__ void keep4(float* p, const Frag<float>& f, int half) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{f.v[4 * half], f.v[4 * half + 1], f.v[4 * half + 2], f.v[4 * half + 3]};
+}
+
 // Lanes of a wave hand each other data through LDS.  A wave's accesses to LDS
 // complete in their order; this keeps the compiler to that order.
 __device__ __forceinline__ void handover() {
@@ -287,8 +308,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void shrink_kernel(gspn_adapter s, 
 // ---------------------------------------------------------------- expand
 // STEPS: steps of 32 ranks whose v a wave keeps for all its columns; 0: any
 // number, one or two steps at a time, v is read again for every 64 columns.
-// EIGHTS: r is a multiple of 8.
-template <typename T, int STEPS, bool EIGHTS>
+// PIECE: 8 or 4 where r is a multiple of it (b comes in pieces of that many
+// elements, a wave's 64 columns as one stretch of memory), else 1 (a column a lane).
+template <typename T, int STEPS, int PIECE>
 __global__ __launch_bounds__(kWaves * 64, 2) void expand_kernel(gspn_adapter s, Launch la) {
     constexpr int kSteps = STEPS ? STEPS : sizeof(T) == 2 ? 2 : 1;
     constexpr int kPitch = 32 * kSteps + 16 / sizeof(T);   // of b's rows in LDS
@@ -297,6 +319,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void expand_kernel(gspn_adapter s, 
     static_assert(kStage >= 16 * kOPitch * 4, "the sums take b's place");
     constexpr int kLoads = 4 * kSteps;                     // pieces of eight elements of b for a lane
     constexpr int kOut = 16 * 64 * sizeof(T) / 1024;       // 16-byte pieces of base for a lane
+    constexpr int kAhead = STEPS == 1 ? 3 : 2;             // columns' worth of base that are on their way
     constexpr int kPer = 16 / sizeof(T);                   // elements of such a piece
     __shared__ __attribute__((aligned(16))) char lds[kWaves * kStage];
     typedef typename Piece<T>::x4 Out;
@@ -348,88 +371,119 @@ __global__ __launch_bounds__(kWaves * 64, 2) void expand_kernel(gspn_adapter s, 
         for (int e = 0; e < 4; ++e) f.set(e, scale * lo[e]), f.set(4 + e, scale * hi[e]);
         return f;
     };
-    Parts<T> v[kSteps];
-#pragma unroll
-    for (int k = 0; k < STEPS; ++k) v[k] = load_v(k);
-
     // b of 64 columns and up to 32 kSteps ranks from rank j0 on: rows of LDS,
-    // zeros behind the last rank
+    // zeros behind the last rank.  All ranks (STEPS != 0) of 64 columns are one
+    // stretch of memory.
+    constexpr int kPart = PIECE > 1 ? PIECE : 8;
+    constexpr int kParts = kLoads * 8 / kPart;   // pieces for a lane, at most
     const T* __restrict__ bp = static_cast<const T*>(s.b) + id * s.M * s.r;
     Frag<T> b[kLoads];
-    auto load_b = [&](int64_t m, int64_t j0) {
-        const int64_t ranks = s.r - j0 < 32 * kSteps ? s.r - j0 : 32 * kSteps;
-        const int pieces = (int)(ranks / 8);
+    int place[STEPS && PIECE > 1 ? kParts : 1];   // where in LDS a lane's pieces go
+    if constexpr (STEPS != 0 && PIECE > 1) {
+        const int pieces = (int)s.r / PIECE;   // of a column
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            if (i >= pieces) break;
+        for (int i = 0; i < kParts; ++i) {
             const int e = i * 64 + lane;
-            const int64_t o = m + e / pieces;   // columns behind the last read it again
-            b[i] = load8(bp + (o < s.M ? o : s.M - 1) * s.r + j0 + 8 * (e % pieces));
+            place[i] = (e / pieces) * kPitch + PIECE * (e % pieces);
+        }
+    }
+    auto load_b = [&](int64_t m, int64_t j0) {
+        const int ranks = (int)(s.r - j0 < 32 * kSteps ? s.r - j0 : 32 * kSteps);
+        const int pieces = ranks / kPart;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            if (i < pieces) {
+                const int e = i * 64 + lane;
+                int64_t at;   // columns behind the last read what is in front of them
+                if constexpr (STEPS != 0) {
+                    at = m * s.r + (int64_t)e * PIECE;
+                    if (at > s.M * s.r - PIECE) at = s.M * s.r - PIECE;
+                } else {
+                    const int64_t o = m + e / pieces;
+                    at = (o < s.M ? o : s.M - 1) * s.r + j0 + PIECE * (e % pieces);
+                }
+                if constexpr (PIECE == 8) b[i] = load8(bp + at);
+                else load4(b[i / 2], i % 2, bp + at);
+            }
         }
     };
     auto keep_b = [&](int64_t m, int64_t j0) {
-        const int64_t ranks = s.r - j0 < 32 * kSteps ? s.r - j0 : 32 * kSteps;
-        if constexpr (EIGHTS) {
-            const int pieces = (int)(ranks / 8);
+        const int ranks = (int)(s.r - j0 < 32 * kSteps ? s.r - j0 : 32 * kSteps);
+        if constexpr (PIECE > 1) {
+            const int pieces = ranks / PIECE;
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                if (i >= pieces) break;
-                const int e = i * 64 + lane;
-                keep8(bs + (e / pieces) * kPitch + 8 * (e % pieces), b[i]);
+            for (int i = 0; i < kParts; ++i) {
+                if (i < pieces) {
+                    const int e = i * 64 + lane;
+                    T* p = bs + (STEPS ? place[STEPS ? i : 0] : (e / pieces) * kPitch + PIECE * (e % pieces));
+                    if constexpr (PIECE == 8) keep8(p, b[i]);
+                    else keep4(p, b[i / 2], i % 2);
+                }
             }
-            // a step's empty pieces (the sums before this tile lay here)
-            for (int p = pieces + q; p < (pieces + 3) / 4 * 4; p += 4) {
-                Frag<T> none;
-                zero(none);
+            // zeros in the rest of a step (the sums before this tile lay here)
+            Frag<T> none;
+            zero(none);
+            for (int j = ranks + PIECE * q; j < (ranks + 31) / 32 * 32; j += 4 * PIECE)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) keep8(bs + (16 * i + c) * kPitch + 8 * p, none);
-            }
+                for (int i = 0; i < 4; ++i) {
+                    T* p = bs + (16 * i + c) * kPitch + j;
+                    if constexpr (PIECE == 8) keep8(p, none);
+                    else keep4(p, none, 0);
+                }
         } else {
-            // one column a lane; columns behind the last read it again
-            const int64_t o = m + lane < s.M ? m + lane : s.M - 1;
+            const int64_t o = m + lane < s.M ? m + lane : s.M - 1;   // columns behind the last read it again
             const T* __restrict__ p = bp + o * s.r + j0;
-            for (int64_t j = 0; j < (ranks + 31) / 32 * 32; j += 8) keep8(bs + lane * kPitch + j, load8(p + j, ranks - j));
+            for (int j = 0; j < (ranks + 31) / 32 * 32; j += 8) keep8(bs + lane * kPitch + j, load8(p + j, ranks - j));
         }
     };
     // base of 16 rows of 64 columns, in pieces of whole rows
     constexpr int kLine = 64 / kPer;   // lanes of a row
     const int oc = (lane % kLine) * kPer, orow = lane / kLine;
-    Out old[kOut];
-    auto load_base = [&](int64_t m) {
+    Out old[kAhead][kOut];
+    auto load_base = [&](int slot, int64_t m) {
+        if (m >= last) return;
 #pragma unroll
         for (int i = 0; i < kOut; ++i) {
             const int t = i * (64 / kLine) + orow;
             if (t < mine && m + oc + kPer <= s.M)
-                old[i] = *reinterpret_cast<const Out*>(base + (row + t) * s.base_stride + m + oc);
+                old[slot][i] = *reinterpret_cast<const Out*>(base + (row + t) * s.base_stride + m + oc);
         }
     };
-    if constexpr (EIGHTS) load_b(first, 0);
-    load_base(first);
+    if constexpr (PIECE > 1) load_b(first, 0);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load_base(i, first + i * stride);
+    Parts<T> v[kSteps];
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) v[k] = load_v(k);
     for (int64_t m = first; m < last; m += stride) {
         f32x4 acc[4] = {};
         Out now[kOut];
 #pragma unroll
-        for (int i = 0; i < kOut; ++i) now[i] = old[i];
+        for (int i = 0; i < kOut; ++i) {
+            now[i] = old[0][i];
+#pragma unroll
+            for (int a = 1; a < kAhead; ++a) old[a - 1][i] = old[a][i];
+        }
         const bool more = m + stride < last;
         for (int64_t j0 = 0; j0 < (STEPS ? 1 : s.r); j0 += 32 * kSteps) {
             keep_b(m, j0);
             handover();
             if constexpr (STEPS == 0) {
                 const int64_t next = j0 + 32 * kSteps;
-                if constexpr (EIGHTS) {
+                if constexpr (PIECE > 1) {
                     if (next < s.r) load_b(m, next);
                     else if (more) load_b(m + stride, 0);
                 }
-                if (j0 == 0 && more) load_base(m + stride);
+                if (j0 == 0) load_base(kAhead - 1, m + kAhead * stride);
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) v[k] = load_v((int)(j0 / 32) + k);
-            } else if (more) {
-                if constexpr (EIGHTS) load_b(m + stride, 0);
-                load_base(m + stride);
+            } else {
+                if (PIECE > 1 && more) load_b(m + stride, 0);
+                load_base(kAhead - 1, m + kAhead * stride);
             }
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
-                if (j0 + 32 * k >= s.r) break;
+                if (j0 + 32 * k < s.r)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     multiply(acc[i], kept8(bs + (16 * i + c) * kPitch + 32 * k + 8 * q), v[k]);
@@ -499,6 +553,14 @@ Launch plan(const gspn_adapter& s) {
     return la;
 }
 
+template <typename T, int PIECE, typename F>
+void expand_pieces(const gspn_adapter& s, F f) {
+    if (s.r <= 32) f(expand_kernel<T, 1, PIECE>);
+    else if (s.r <= 64) f(expand_kernel<T, 2, PIECE>);
+    else if (sizeof(T) == 2 && s.r <= 128) f(expand_kernel<T, sizeof(T) == 2 ? 4 : 0, PIECE>);
+    else f(expand_kernel<T, 0, PIECE>);
+}
+
 template <typename T>
 void launch_typed(const gspn_adapter& s, const Launch& la, hipStream_t stream) {
     const dim3 gs(la.total * la.groups * la.splits), ge(la.total * la.parts);
@@ -507,10 +569,9 @@ void launch_typed(const gspn_adapter& s, const Launch& la, hipStream_t stream) {
     if (s.r <= 16) shrink(shrink_kernel<T, 1>);
     else if (s.r <= 32) shrink(shrink_kernel<T, 2>);
     else shrink(shrink_kernel<T, 4>);
-    const bool eights = s.r % 8 == 0;
-    if (s.r <= 32) eights ? expand(expand_kernel<T, 1, true>) : expand(expand_kernel<T, 1, false>);
-    else if (s.r <= 64) eights ? expand(expand_kernel<T, 2, true>) : expand(expand_kernel<T, 2, false>);
-    else eights ? expand(expand_kernel<T, 0, true>) : expand(expand_kernel<T, 0, false>);
+    if (s.r % 8 == 0) expand_pieces<T, 8>(s, expand);
+    else if (s.r % 4 == 0) expand_pieces<T, 4>(s, expand);
+    else expand_pieces<T, 1>(s, expand);
 }
 
 }  // namespace
