@@ -185,7 +185,19 @@ __device__ __forceinline__ void multiply(f32x4& c, const Frag<uint16_t>& a, cons
 }
 __device__ __forceinline__ void multiply(f32x4& c, const Frag<float>& a, const Parts<float>& b) { multiply(c, a, b.hi); }
 
+// What shrink_kernel finds out about a tile and expand_kernel reads back in one
+// load (finding the tile, its adapter and its scale takes four that wait for
+// each other).
+struct __attribute__((aligned(16))) TileNote {
+    int32_t row, count;   // first row, rows (0: nothing to do)
+    int32_t id;           // the adapter, kNone or kTail
+    float scale;
+};
+constexpr int32_t kNone = -1, kTail = -2;   // a request without an adapter; rows of no request
+
 struct Launch {
+    TileNote* notes;    // [total]
+    float* v;           // [splits][T][pitch]
     uint32_t tiles;     // of a request (rows of equal length), else 0
     uint32_t total;     // of all
     uint32_t groups;    // shrink: groups of kRanks ranks
@@ -213,11 +225,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void shrink_kernel(gspn_adapter s, 
     const uint32_t group = rest % la.groups, w = rest / la.groups;
     const Tile tile = find_tile<kRows>(s.offsets, s.T, s.N, la.tiles, w, lane);
     const int64_t start = tile.j * kRows;
-    if (tile.n == s.N || start >= tile.rows) return;
-    const int64_t id = s.ids[tile.n];
-    if (id < 0 || id >= s.R) return;
-    const int count = uniform((int)(tile.rows - start < kRows ? tile.rows - start : kRows));
+    const int64_t left = tile.rows - start;
+    const int count = uniform((int)(left < 0 ? 0 : left < kRows ? left : kRows));
     const int64_t row = tile.row + start;
+    int64_t id = tile.n == s.N ? kTail : s.ids[tile.n];
+    if (tile.n != s.N && (id < 0 || id >= s.R)) id = kNone;
+    if (split == 0 && group == 0 && threadIdx.x == 0)
+        la.notes[w] = TileNote{(int32_t)row, count, (int32_t)id, id >= 0 && s.scale ? s.scale[id] : 1.0f};
+    if (count == 0 || id < 0) return;
     const int64_t end = ((int64_t)split + 1) * la.slice < s.K ? ((int64_t)split + 1) * la.slice : s.K;
     f32x4* sums = reinterpret_cast<f32x4*>(lds);    // [kWaves][kRB * RB][64]
 
@@ -289,7 +304,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void shrink_kernel(gspn_adapter s, 
     if (count <= 16) products(std::integral_constant<int, 1>());
     else products(std::integral_constant<int, kRB>());
     __syncthreads();
-    float* __restrict__ v = static_cast<float*>(s.work) + (size_t)split * s.T * la.pitch;
+    float* __restrict__ v = la.v + (size_t)split * s.T * la.pitch;
     for (int b = wave; b < kRB * RB; b += kWaves) {
         const int t = (b / RB) * 16 + c, i = b % RB;
         if (t >= count) continue;
@@ -309,54 +324,56 @@ __global__ __launch_bounds__(kWaves * 64, 2) void shrink_kernel(gspn_adapter s, 
 // STEPS: steps of 32 ranks whose v a wave keeps for all its columns; 0: any
 // number, one or two steps at a time, v is read again for every 64 columns.
 // PIECE: 8 or 4 where r is a multiple of it (b comes in pieces of that many
-// elements, a wave's 64 columns as one stretch of memory), else 1 (a column a lane).
+// elements, 64 columns as one stretch of memory), else 1 (a column a lane).
+//
+// The waves of a tile of more than 16 rows have 16 rows each and walk the same
+// columns: each brings a quarter of b's and they share it (two buffers, a
+// barrier a turn).  The waves of up to 16 rows have columns of their own.
 template <typename T, int STEPS, int PIECE>
 __global__ __launch_bounds__(kWaves * 64, 2) void expand_kernel(gspn_adapter s, Launch la) {
     constexpr int kSteps = STEPS ? STEPS : sizeof(T) == 2 ? 2 : 1;
     constexpr int kPitch = 32 * kSteps + 16 / sizeof(T);   // of b's rows in LDS
     constexpr int kOPitch = 64 + 4;                        // of a row of sums, fp32
-    constexpr int kStage = 64 * kPitch * sizeof(T);        // bytes of LDS of a wave; the sums take b's place
-    static_assert(kStage >= 16 * kOPitch * 4, "the sums take b's place");
-    constexpr int kLoads = 4 * kSteps;                     // pieces of eight elements of b for a lane
+    constexpr int kStage = 64 * kPitch * sizeof(T);        // bytes of LDS of 64 columns of b
+    constexpr int kSums = 16 * kOPitch * 4;                // of a wave's sums
+    static_assert(kStage >= kSums, "the sums take the place of a wave's own b");
+    constexpr int kLds = kWaves * kStage > 2 * kStage + kWaves * kSums ? kWaves * kStage : 2 * kStage + kWaves * kSums;
+    constexpr int kPart = PIECE > 1 ? PIECE : 8;
     constexpr int kOut = 16 * 64 * sizeof(T) / 1024;       // 16-byte pieces of base for a lane
-    constexpr int kAhead = STEPS == 1 ? 3 : 2;             // columns' worth of base that are on their way
     constexpr int kPer = 16 / sizeof(T);                   // elements of such a piece
-    __shared__ __attribute__((aligned(16))) char lds[kWaves * kStage];
+    constexpr int kAhead = 2;                              // turns' worth of base that are on their way
+    __shared__ __attribute__((aligned(16))) char lds[kLds];
     typedef typename Piece<T>::x4 Out;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int q = lane >> 4, c = lane & 15;
     const uint32_t part = blockIdx.x % la.parts, w = blockIdx.x / la.parts;
-    const Tile tile = find_tile<kRows>(s.offsets, s.T, s.N, la.tiles, w, lane);
-    const int64_t start = tile.j * kRows;
-    if (start >= tile.rows) return;
-    const int count = uniform((int)(tile.rows - start < kRows ? tile.rows - start : kRows));
+    const TileNote note = la.notes[w];
+    const int count = uniform(note.count);
+    const int64_t id = uniform(note.id);
+    if (count == 0) return;
     const T* base = static_cast<const T*>(s.base);   // may be out itself: a lane reads what it then writes
     T* out = static_cast<T*>(s.out);
-    // the waves of up to 16 rows share the columns, those of more have 16 rows each
     int64_t first = part * la.columns;
     const int64_t last = first + la.columns < s.M ? first + la.columns : s.M;
-    int block = wave, stride = 64;
-    if (count <= 16) block = 0, first += 64 * wave, stride = 64 * kWaves;
-    const int mine = count - block * 16 < 16 ? count - block * 16 : 16;   // rows of this wave
-    if (mine <= 0 || first >= last) return;
-    const int64_t row = tile.row + start + block * 16;
-    const int64_t id = tile.n == s.N ? -1 : s.ids[tile.n];
-    if (tile.n == s.N || id < 0 || id >= s.R) {
+    const int block = count <= 16 ? 0 : wave, stride = count <= 16 ? 64 * kWaves : 64;
+    if (count <= 16) first += 64 * wave;
+    const int mine = count - block * 16 < 16 ? count - block * 16 : 16;   // rows of this wave, if any
+    const int64_t row = uniform(note.row) + block * 16;
+    if (id < 0) {
         // rows of no request (zero, or as they were), or of one without an adapter (base's)
-        if (tile.n == s.N ? !(s.flags & GSPN_SEQ_ZERO_TAIL) : base == out) return;
+        if (id == kTail ? !(s.flags & GSPN_SEQ_ZERO_TAIL) : base == out) return;
         for (int t = 0; t < mine; ++t)
             for (int64_t m = first + lane; m < last; m += stride)
                 out[(row + t) * s.out_stride + m] =
-                    tile.n == s.N ? from_f32(0.0f, (T*)nullptr) : base[(row + t) * s.base_stride + m];
+                    id == kTail ? from_f32(0.0f, (T*)nullptr) : base[(row + t) * s.base_stride + m];
         return;
     }
-    T* bs = reinterpret_cast<T*>(lds + wave * kStage);
-    float* os = reinterpret_cast<float*>(lds + wave * kStage);
-    const float scale = s.scale ? s.scale[id] : 1.0f;
+    const T* __restrict__ bp = static_cast<const T*>(s.b) + id * s.M * s.r;
+    const float scale = note.scale;
     // v of the lane's row, ranks 32 k + 8 q .. + 7: the splits' sums, scaled
     // (rows behind the last read it again)
     const float* __restrict__ vp =
-        static_cast<const float*>(s.work) + (size_t)(row + (c < mine ? c : mine - 1)) * la.pitch + 8 * q;
+        la.v + (size_t)(row + (c < mine ? c : mine - 1)) * la.pitch + 8 * q;
     auto load_v = [&](int k) {
         f32x4 lo = {}, hi = {};
         if (32 * k + 8 * q < la.pitch) {
@@ -371,168 +388,170 @@ __global__ __launch_bounds__(kWaves * 64, 2) void expand_kernel(gspn_adapter s, 
         for (int e = 0; e < 4; ++e) f.set(e, scale * lo[e]), f.set(4 + e, scale * hi[e]);
         return f;
     };
-    // b of 64 columns and up to 32 kSteps ranks from rank j0 on: rows of LDS,
-    // zeros behind the last rank.  All ranks (STEPS != 0) of 64 columns are one
-    // stretch of memory.
-    constexpr int kPart = PIECE > 1 ? PIECE : 8;
-    constexpr int kParts = kLoads * 8 / kPart;   // pieces for a lane, at most
-    const T* __restrict__ bp = static_cast<const T*>(s.b) + id * s.M * s.r;
-    Frag<T> b[kLoads];
-    int place[STEPS && PIECE > 1 ? kParts : 1];   // where in LDS a lane's pieces go
-    if constexpr (STEPS != 0 && PIECE > 1) {
-        const int pieces = (int)s.r / PIECE;   // of a column
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) {
-            const int e = i * 64 + lane;
-            place[i] = (e / pieces) * kPitch + PIECE * (e % pieces);
-        }
-    }
-    auto load_b = [&](int64_t m, int64_t j0) {
-        const int ranks = (int)(s.r - j0 < 32 * kSteps ? s.r - j0 : 32 * kSteps);
-        const int pieces = ranks / kPart;
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) {
-            if (i < pieces) {
-                const int e = i * 64 + lane;
-                int64_t at;   // columns behind the last read what is in front of them
-                if constexpr (STEPS != 0) {
-                    at = m * s.r + (int64_t)e * PIECE;
-                    if (at > s.M * s.r - PIECE) at = s.M * s.r - PIECE;
-                } else {
-                    const int64_t o = m + e / pieces;
-                    at = (o < s.M ? o : s.M - 1) * s.r + j0 + PIECE * (e % pieces);
-                }
-                if constexpr (PIECE == 8) b[i] = load8(bp + at);
-                else load4(b[i / 2], i % 2, bp + at);
-            }
-        }
-    };
-    auto keep_b = [&](int64_t m, int64_t j0) {
-        const int ranks = (int)(s.r - j0 < 32 * kSteps ? s.r - j0 : 32 * kSteps);
-        if constexpr (PIECE > 1) {
-            const int pieces = ranks / PIECE;
-#pragma unroll
-            for (int i = 0; i < kParts; ++i) {
-                if (i < pieces) {
-                    const int e = i * 64 + lane;
-                    T* p = bs + (STEPS ? place[STEPS ? i : 0] : (e / pieces) * kPitch + PIECE * (e % pieces));
-                    if constexpr (PIECE == 8) keep8(p, b[i]);
-                    else keep4(p, b[i / 2], i % 2);
-                }
-            }
-            // zeros in the rest of a step (the sums before this tile lay here)
-            Frag<T> none;
-            zero(none);
-            for (int j = ranks + PIECE * q; j < (ranks + 31) / 32 * 32; j += 4 * PIECE)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    T* p = bs + (16 * i + c) * kPitch + j;
-                    if constexpr (PIECE == 8) keep8(p, none);
-                    else keep4(p, none, 0);
-                }
-        } else {
-            const int64_t o = m + lane < s.M ? m + lane : s.M - 1;   // columns behind the last read it again
-            const T* __restrict__ p = bp + o * s.r + j0;
-            for (int j = 0; j < (ranks + 31) / 32 * 32; j += 8) keep8(bs + lane * kPitch + j, load8(p + j, ranks - j));
-        }
-    };
     // base of 16 rows of 64 columns, in pieces of whole rows
     constexpr int kLine = 64 / kPer;   // lanes of a row
     const int oc = (lane % kLine) * kPer, orow = lane / kLine;
-    Out old[kAhead][kOut];
-    auto load_base = [&](int slot, int64_t m) {
-        if (m >= last) return;
+
+    auto walk = [&](auto shared) {
+        constexpr bool SHARED = decltype(shared)::value;
+        constexpr int kBring = 4 * kSteps * 8 / kPart / (SHARED ? kWaves : 1);   // pieces of b for a lane, at most
+        const int from = SHARED ? wave : 0, by = SHARED ? kWaves : 1;
+        float* os = reinterpret_cast<float*>(SHARED ? lds + 2 * kStage + wave * kSums : lds + wave * kStage);
+        Frag<T> b[kBring * kPart / 8 > 0 ? kBring * kPart / 8 : 1];
+        int place[STEPS && PIECE > 1 ? kBring : 1];   // where in LDS a lane's pieces go
+        if constexpr (STEPS != 0 && PIECE > 1) {
+            const int pieces = (int)s.r / PIECE;   // of a column
 #pragma unroll
-        for (int i = 0; i < kOut; ++i) {
-            const int t = i * (64 / kLine) + orow;
-            if (t < mine && m + oc + kPer <= s.M)
-                old[slot][i] = *reinterpret_cast<const Out*>(base + (row + t) * s.base_stride + m + oc);
+            for (int i = 0; i < kBring; ++i) {
+                const int e = (i * by + from) * 64 + lane;
+                place[i] = (e / pieces) * kPitch + PIECE * (e % pieces);
+            }
         }
-    };
-    if constexpr (PIECE > 1) load_b(first, 0);
+        // 64 columns of b and up to 32 kSteps ranks from rank j0 on
+        auto load_b = [&](int64_t m, int64_t j0) {
+            const int ranks = (int)(s.r - j0 < 32 * kSteps ? s.r - j0 : 32 * kSteps);
+            const int pieces = ranks / kPart;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) load_base(i, first + i * stride);
-    Parts<T> v[kSteps];
+            for (int i = 0; i < kBring; ++i) {
+                if (i * by + from < pieces) {
+                    const int e = (i * by + from) * 64 + lane;
+                    int64_t at;   // columns behind the last read what is in front of them
+                    if constexpr (STEPS != 0) {
+                        at = m * s.r + (int64_t)e * PIECE;
+                        if (at > s.M * s.r - PIECE) at = s.M * s.r - PIECE;
+                    } else {
+                        const int64_t o = m + e / pieces;
+                        at = (o < s.M ? o : s.M - 1) * s.r + j0 + PIECE * (e % pieces);
+                    }
+                    if constexpr (PIECE == 8) b[i] = load8(bp + at);
+                    else load4(b[i / 2], i % 2, bp + at);
+                }
+            }
+        };
+        // into rows of LDS, zeros behind the last rank
+        auto keep_b = [&](T* bs, int64_t m, int64_t j0) {
+            const int ranks = (int)(s.r - j0 < 32 * kSteps ? s.r - j0 : 32 * kSteps);
+            if constexpr (PIECE > 1) {
+                const int pieces = ranks / PIECE;
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k) v[k] = load_v(k);
-    for (int64_t m = first; m < last; m += stride) {
-        f32x4 acc[4] = {};
-        Out now[kOut];
+                for (int i = 0; i < kBring; ++i) {
+                    if (i * by + from < pieces) {
+                        const int e = (i * by + from) * 64 + lane;
+                        T* p = bs + (STEPS ? place[STEPS ? i : 0] : (e / pieces) * kPitch + PIECE * (e % pieces));
+                        if constexpr (PIECE == 8) keep8(p, b[i]);
+                        else keep4(p, b[i / 2], i % 2);
+                    }
+                }
+                Frag<T> none;
+                zero(none);
+                for (int j = ranks + PIECE * q; j < (ranks + 31) / 32 * 32; j += 4 * PIECE)
 #pragma unroll
-        for (int i = 0; i < kOut; ++i) {
-            now[i] = old[0][i];
+                    for (int i = 0; i < 4; ++i) {
+                        if (SHARED && i != wave) continue;
+                        T* p = bs + (16 * i + c) * kPitch + j;
+                        if constexpr (PIECE == 8) keep8(p, none);
+                        else keep4(p, none, 0);
+                    }
+            } else {
+                const int64_t o = m + lane < s.M ? m + lane : s.M - 1;   // columns behind the last read it again
+                const T* __restrict__ p = bp + o * s.r + j0;
+                for (int j = 8 * from; j < (ranks + 31) / 32 * 32; j += 8 * by)
+                    keep8(bs + lane * kPitch + j, load8(p + j, ranks - j));
+            }
+        };
+        Out old[kAhead][kOut];
+        auto load_base = [&](int slot, int64_t m) {
+            if (m >= last) return;
 #pragma unroll
-            for (int a = 1; a < kAhead; ++a) old[a - 1][i] = old[a][i];
-        }
-        const bool more = m + stride < last;
-        for (int64_t j0 = 0; j0 < (STEPS ? 1 : s.r); j0 += 32 * kSteps) {
-            keep_b(m, j0);
-            handover();
-            if constexpr (STEPS == 0) {
+            for (int i = 0; i < kOut; ++i) {
+                const int t = i * (64 / kLine) + orow;
+                if (t < mine && m + oc + kPer <= s.M)
+                    old[slot][i] = *reinterpret_cast<const Out*>(base + (row + t) * s.base_stride + m + oc);
+            }
+        };
+        if constexpr (PIECE > 1) load_b(first, 0);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load_base(i, first + i * stride);
+        Parts<T> v[kSteps];
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) v[k] = load_v(k);
+        int buffer = 0;
+        for (int64_t m = first; m < last; m += stride) {
+            f32x4 acc[4] = {};
+            Out now[kOut];
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) {
+                now[i] = old[0][i];
+#pragma unroll
+                for (int a = 1; a < kAhead; ++a) old[a - 1][i] = old[a][i];
+            }
+            const bool more = m + stride < last;
+            for (int64_t j0 = 0; j0 < (STEPS ? 1 : s.r); j0 += 32 * kSteps, buffer ^= 1) {
+                T* bs = reinterpret_cast<T*>(lds + (SHARED ? buffer : wave) * kStage);
+                keep_b(bs, m, j0);
+                if constexpr (SHARED) __syncthreads();
+                else handover();
                 const int64_t next = j0 + 32 * kSteps;
                 if constexpr (PIECE > 1) {
-                    if (next < s.r) load_b(m, next);
+                    if (STEPS == 0 && next < s.r) load_b(m, next);
                     else if (more) load_b(m + stride, 0);
                 }
                 if (j0 == 0) load_base(kAhead - 1, m + kAhead * stride);
+                if constexpr (STEPS == 0) {
 #pragma unroll
-                for (int k = 0; k < kSteps; ++k) v[k] = load_v((int)(j0 / 32) + k);
-            } else {
-                if (PIECE > 1 && more) load_b(m + stride, 0);
-                load_base(kAhead - 1, m + kAhead * stride);
+                    for (int k = 0; k < kSteps; ++k) v[k] = load_v((int)(j0 / 32) + k);
+                }
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k)
+                    if (j0 + 32 * k < s.r)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            multiply(acc[i], kept8(bs + (16 * i + c) * kPitch + 32 * k + 8 * q), v[k]);
+                handover();
             }
+            // lane l holds row c of the columns 16 i + 4 q .. + 3
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                if (j0 + 32 * k < s.r)
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(os + c * kOPitch + 16 * i + 4 * q) = acc[i];
+            handover();
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    multiply(acc[i], kept8(bs + (16 * i + c) * kPitch + 32 * k + 8 * q), v[k]);
+            for (int i = 0; i < kOut; ++i) {
+                const int t = i * (64 / kLine) + orow;
+                float sum[kPer];
+#pragma unroll
+                for (int e = 0; e < kPer; e += 4) {
+                    const f32x4 f = *reinterpret_cast<const f32x4*>(os + t * kOPitch + oc + e);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sum[e + k] = f[k];
+                }
+                if (t >= mine) continue;
+                const int64_t left = s.M - m - oc;
+                T* po = out + (row + t) * s.out_stride + m + oc;
+                if (left >= kPer) {
+                    Out o;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (sizeof(T) == 2)
+                            o[e] = pack_bf16x2(bf16_lo(now[i][e]) + sum[2 * e], bf16_hi(now[i][e]) + sum[2 * e + 1]);
+                        else
+                            o[e] = now[i][e] + sum[e];
+                    }
+                    *reinterpret_cast<Out*>(po) = o;
+                } else {
+                    const T* pb = base + (row + t) * s.base_stride + m + oc;
+#pragma unroll
+                    for (int e = 0; e < kPer - 1; ++e)
+                        if (e < left) po[e] = from_f32(to_f32(pb[e]) + sum[e], (T*)nullptr);
+                }
             }
             handover();
         }
-        // lane l holds row c of the columns 16 i + 4 q .. + 3
-#pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(os + c * kOPitch + 16 * i + 4 * q) = acc[i];
-        handover();
-#pragma unroll
-        for (int i = 0; i < kOut; ++i) {
-            const int t = i * (64 / kLine) + orow;
-            float sum[kPer];
-#pragma unroll
-            for (int e = 0; e < kPer; e += 4) {
-                const f32x4 f = *reinterpret_cast<const f32x4*>(os + t * kOPitch + oc + e);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sum[e + k] = f[k];
-            }
-            if (t >= mine) continue;
-            const int64_t left = s.M - m - oc;
-            T* po = out + (row + t) * s.out_stride + m + oc;
-            if (left >= kPer) {
-                if constexpr (sizeof(T) == 2) {
-                    Out o;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[e] = pack_bf16x2(bf16_lo(now[i][e]) + sum[2 * e], bf16_hi(now[i][e]) + sum[2 * e + 1]);
-                    *reinterpret_cast<Out*>(po) = o;
-                } else {
-                    Out o;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = now[i][e] + sum[e];
-                    *reinterpret_cast<Out*>(po) = o;
-                }
-            } else {
-                const T* pb = base + (row + t) * s.base_stride + m + oc;
-#pragma unroll
-                for (int e = 0; e < kPer - 1; ++e)
-                    if (e < left) po[e] = from_f32(to_f32(pb[e]) + sum[e], (T*)nullptr);
-            }
-        }
-        handover();
-    }
+    };
+    if (count <= 16) walk(std::integral_constant<bool, false>());
+    else walk(std::integral_constant<bool, true>());
 }
 
 // ---------------------------------------------------------------- host
-// Sizes of the launches; the workspace holds [splits][T][pitch] fp32.
+// Sizes of the launches; the workspace holds the tiles' notes and v.
 Launch plan(const gspn_adapter& s) {
     Launch la;
     la.tiles = s.offsets ? 0 : tiles_of_sequence<kRows>(s.T, s.N);
@@ -550,6 +569,8 @@ Launch plan(const gspn_adapter& s) {
     while (columns < 1024 && la.total * ((s.M + columns - 1) / columns) > 2048) columns *= 2;
     la.columns = columns;
     la.parts = (uint32_t)((s.M + columns - 1) / columns);
+    la.notes = static_cast<TileNote*>(s.work);
+    la.v = reinterpret_cast<float*>(la.notes + la.total);
     return la;
 }
 
@@ -578,7 +599,7 @@ void launch_typed(const gspn_adapter& s, const Launch& la, hipStream_t stream) {
 
 int64_t adapter_workspace(const gspn_adapter& s) {
     const Launch la = plan(s);
-    return (int64_t)la.splits * s.T * la.pitch * 4;
+    return (int64_t)la.total * (int64_t)sizeof(TileNote) + (int64_t)la.splits * s.T * la.pitch * 4;
 }
 
 hipError_t launch_adapter(const gspn_adapter& s, hipStream_t stream) {
