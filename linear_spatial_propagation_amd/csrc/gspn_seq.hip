@@ -688,42 +688,100 @@ __global__ __launch_bounds__(256) void seq_clear_kernel(uint4* __restrict__ coun
 }
 
 // ---------------------------------------------------------------- step
-// One lane per channel of a row.  Rows of one slot are taken in their order
-// by the lanes of the first of them; the others leave it to those.
-template <typename T>
-__global__ __launch_bounds__(256) void seq_step_kernel(gspn_seq_token s) {
-    const int64_t blocks = (s.D + 255) / 256;
-    const int64_t row = blockIdx.x / blocks;
-    const int64_t d = (blockIdx.x - row * blocks) * 256 + threadIdx.x;
+// V channels of a row: 16 bytes of state and 8 or 16 of the others where V is 4.
+template <typename T> struct Four;
+template <> struct Four<uint16_t> { typedef uint32_t type __attribute__((ext_vector_type(2))); };
+template <> struct Four<float> { typedef float type __attribute__((ext_vector_type(4))); };
+
+template <typename T, int V> __device__ __forceinline__ void get(const T* p, float (&v)[V]) {
+    if constexpr (V == 1) {
+        v[0] = to_f32(*p);
+    } else {
+        const typename Four<T>::type r = *reinterpret_cast<const typename Four<T>::type*>(p);
+        if constexpr (sizeof(T) == 2) v[0] = bf16_lo(r.x), v[1] = bf16_hi(r.x), v[2] = bf16_lo(r.y), v[3] = bf16_hi(r.y);
+        else v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+    }
+}
+template <typename T, int V> __device__ __forceinline__ void set(T* p, const float (&v)[V]) {
+    if constexpr (V == 1) {
+        *p = from_f32(v[0], p);
+    } else {
+        typename Four<T>::type r;
+        if constexpr (sizeof(T) == 2) r.x = pack_bf16x2(v[0], v[1]), r.y = pack_bf16x2(v[2], v[3]);
+        else r.x = v[0], r.y = v[1], r.z = v[2], r.w = v[3];
+        *reinterpret_cast<typename Four<T>::type*>(p) = r;
+    }
+}
+
+// One lane for V channels of a row, read and written once.  What bounds a step
+// is the time of its few accesses behind one another, so a lane asks for all it
+// needs before its workgroup knows whether the row is its own to take: rows of
+// one slot are taken in their order by the lanes of the first of them.
+constexpr int kStepLanes = 256;
+
+template <typename T, int V, bool SHARED>
+__global__ __launch_bounds__(kStepLanes) void seq_step_kernel(gspn_seq_token s, uint32_t blocks) {
+    __shared__ int found[kStepLanes / 64];
+    const uint32_t row = blockIdx.x / blocks;
+    const int64_t d = (int64_t)(blockIdx.x - row * blocks) * (kStepLanes * V) + threadIdx.x * V;
     const int64_t slot = s.slots ? s.slots[row] : row;
+    const bool mine = d < s.D;
     if (slot < 0 || slot >= s.S) {
-        if ((s.flags & GSPN_SEQ_ZERO_TAIL) && d < s.D)
-            static_cast<T*>(s.y)[row * s.y_stride + d] = from_f32(0.0f, (T*)nullptr);
+        const float zero[V] = {};
+        if ((s.flags & GSPN_SEQ_ZERO_TAIL) && mine) set<T, V>(static_cast<T*>(s.y) + row * s.y_stride + d, zero);
         return;
     }
-    bool more = false;
-    if (s.slots) {
-        bool earlier = false, later = false;
-        for (int64_t r = threadIdx.x; r < s.N; r += 256)
-            if (r != row && s.slots[r] == slot) (r < row ? earlier : later) = true;
-        if (__syncthreads_or(earlier)) return;
-        more = __syncthreads_or(later);
+    const uint32_t k = SHARED ? (uint32_t)d / (uint32_t)s.ch_per_weight : (uint32_t)d;
+    float h[V], g[V], x[V], l[V], u[V];
+    auto fetch = [&](int64_t r) {
+        const T* gp = static_cast<const T*>(s.gate) + r * s.gate_stride;
+        if constexpr (!SHARED) {
+            get<T, V>(gp + d, g);
+        } else if (V == 1 || s.ch_per_weight % 4 == 0) {
+            g[0] = to_f32(gp[k]);
+#pragma unroll
+            for (int v = 1; v < V; ++v) g[v] = g[0];
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) g[v] = to_f32(gp[(uint32_t)(d + v) / (uint32_t)s.ch_per_weight]);
+        }
+        get<T, V>(static_cast<const T*>(s.x) + r * s.x_stride + d, x);
+        if (s.lam) get<T, V>(static_cast<const T*>(s.lam) + r * s.lam_stride + d, l);
+        if (s.u) get<T, V>(static_cast<const T*>(s.u) + r * s.u_stride + d, u);
+    };
+    if (mine) {
+        get<float, V>(s.state + slot * s.D + d, h);
+        fetch(row);
     }
-    if (d >= s.D) return;
-    const int64_t k = d / s.ch_per_weight;
-    float h = s.state[slot * s.D + d];
-    for (int64_t r = row; r < s.N; ++r) {
-        if (r != row && s.slots[r] != slot) continue;
-        float most;
-        const float a = gate_of(to_f32(static_cast<const T*>(s.gate)[r * s.gate_stride + k]), most);
-        const float xv = to_f32(static_cast<const T*>(s.x)[r * s.x_stride + d]);
-        const float lv = s.lam ? to_f32(static_cast<const T*>(s.lam)[r * s.lam_stride + d]) : take(a, most);
-        h = keep(a, h, lv, xv);
-        const float uv = s.u ? to_f32(static_cast<const T*>(s.u)[r * s.u_stride + d]) : 1.0f;
-        static_cast<T*>(s.y)[r * s.y_stride + d] = from_f32(uv * h, (T*)nullptr);
-        if (!more) break;
+    int others = 0;   // 1: an earlier row has the slot, 2: a later one
+    if (s.slots && s.N > 1) {
+        for (int64_t r = threadIdx.x; r < s.N; r += kStepLanes)
+            if (r != row && s.slots[r] == slot) others |= r < row ? 1 : 2;
+        const int any = (__ballot(others & 1) ? 1 : 0) | (__ballot(others & 2) ? 2 : 0);
+        if ((threadIdx.x & 63) == 0) found[threadIdx.x >> 6] = any;
+        __syncthreads();
+        others = 0;
+#pragma unroll
+        for (int i = 0; i < kStepLanes / 64; ++i) others |= found[i];
     }
-    s.state[slot * s.D + d] = h;
+    if ((others & 1) || !mine) return;
+    for (int64_t r = row;;) {
+        float y[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float most;
+            const float a = gate_of(g[v], most);
+            h[v] = keep(a, h[v], s.lam ? l[v] : take(a, most), x[v]);
+            y[v] = s.u ? u[v] * h[v] : h[v];
+        }
+        set<T, V>(static_cast<T*>(s.y) + r * s.y_stride + d, y);
+        if (!(others & 2)) break;
+        do ++r;
+        while (r < s.N && s.slots[r] != slot);
+        if (r >= s.N) break;
+        fetch(r);
+    }
+    set<float, V>(s.state + slot * s.D + d, h);
 }
 
 // ---------------------------------------------------------------- host
@@ -905,9 +963,27 @@ hipError_t launch_seq_bwd(const gspn_seq& s, const gspn_seq_grad& g, hipStream_t
 }
 
 hipError_t launch_seq_step(const gspn_seq_token& t, hipStream_t stream) {
-    const dim3 grid((unsigned)(t.N * ((t.D + 255) / 256)));
-    if (t.dtype == GSPN_BF16) hipLaunchKernelGGL(seq_step_kernel<uint16_t>, grid, dim3(256), 0, stream, t);
-    else hipLaunchKernelGGL(seq_step_kernel<float>, grid, dim3(256), 0, stream, t);
+    // four channels a lane where every row of four is a whole 16- or 8-byte piece
+    auto fours = [&](const void* p, int64_t stride, size_t es) {
+        return ((uintptr_t)p & (4 * es - 1)) == 0 && (!p || stride % 4 == 0);
+    };
+    const size_t es = t.dtype == GSPN_BF16 ? 2 : 4;
+    const bool shared = t.ch_per_weight > 1;
+    const int V = t.D % 4 == 0 && fours(t.state, 4, 4) && fours(t.x, t.x_stride, es) && fours(t.lam, t.lam_stride, es) &&
+                          fours(t.u, t.u_stride, es) && fours(t.y, t.y_stride, es) &&
+                          (shared || fours(t.gate, t.gate_stride, es))
+                      ? 4 : 1;
+    const uint32_t blocks = (uint32_t)((t.D + kStepLanes * V - 1) / (kStepLanes * V));
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)t.N * blocks), dim3(kStepLanes), 0, stream, t, blocks);
+    };
+    if (t.dtype == GSPN_BF16) {
+        if (V == 4) shared ? go(seq_step_kernel<uint16_t, 4, true>) : go(seq_step_kernel<uint16_t, 4, false>);
+        else shared ? go(seq_step_kernel<uint16_t, 1, true>) : go(seq_step_kernel<uint16_t, 1, false>);
+    } else {
+        if (V == 4) shared ? go(seq_step_kernel<float, 4, true>) : go(seq_step_kernel<float, 4, false>);
+        else shared ? go(seq_step_kernel<float, 1, true>) : go(seq_step_kernel<float, 1, false>);
+    }
     return hipGetLastError();
 }
 
