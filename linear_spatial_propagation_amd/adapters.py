@@ -2,10 +2,21 @@
 (gspn_adapter_add of include/gspn.h)."""
 from __future__ import annotations
 
+import functools
+
 from . import _lib
 from .sequence import _call, _code, _index, _layout, _like, _row_stride
 
 _PACK = _lib.packer(_lib.Adapter)
+
+
+@functools.lru_cache(maxsize=4096)
+def _work_bytes(T, K, M, N, R, r, code, packed):
+    need = _lib.load().gspn_adapter_workspace(_PACK(0, 0, 0, 0, 0, 0, int(packed), 0, 0, 0, T, K, M, N, R, r, 0, 0, 0,
+                                                    code, 0))
+    if need < 0:
+        _lib.check(need)
+    return need
 
 
 def adapter_add(base, x, a, b, ids, *, scale=None, offsets=None, out=None):
@@ -36,14 +47,15 @@ def adapter_add(base, x, a, b, ids, *, scale=None, offsets=None, out=None):
         raise ValueError("a must be [R, r, K], b [R, M, r], and base laid out like x")
     R, r, K = a.shape
     M = base.shape[-1]
-    for name, t, shape in (("a", a, (R, r, x.shape[-1])), ("b", b, (R, M, r))):
-        if t.device != x.device or t.dtype != x.dtype:
-            raise ValueError(f"{name} must share x's device and dtype")
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (base, x, a, b, scale)):
+    if a.device != x.device or b.device != x.device or a.dtype != x.dtype or b.dtype != x.dtype:
+        raise ValueError("a and b must share x's device and dtype")
+    if K != x.shape[-1] or b.shape != (R, M, r):
+        raise ValueError(f"a and b have shapes {tuple(a.shape)} and {tuple(b.shape)}, expected [R, r, {x.shape[-1]}] and "
+                         f"[R, {M}, r]")
+    if not (a.is_contiguous() and b.is_contiguous()):
+        raise ValueError("a and b must be contiguous")
+    if torch.is_grad_enabled() and (base.requires_grad or x.requires_grad or a.requires_grad or b.requires_grad or
+                                    (scale is not None and scale.requires_grad)):
         raise RuntimeError("adapter_add has no backward; call it under torch.no_grad()")
     dev, code = x.device, _code(x)
     px, sx = x.data_ptr(), _row_stride("x", x)
@@ -59,9 +71,7 @@ def adapter_add(base, x, a, b, ids, *, scale=None, offsets=None, out=None):
         out = torch.empty(base.shape, dtype=x.dtype, device=dev)
     py, sy = _like("out", out, x, base.shape)
     lib = _lib.load()
-    need = lib.gspn_adapter_workspace(_PACK(0, 0, 0, 0, 0, 0, po, 0, 0, 0, T, K, M, N, R, r, 0, 0, 0, code, 0))
-    if need < 0:
-        _lib.check(need)
+    need = _work_bytes(T, K, M, N, R, r, code, po != 0)
     work = torch.empty(need, dtype=torch.uint8, device=dev)
     _call(lib.gspn_adapter_add, dev, _PACK(pb, px, a.data_ptr(), b.data_ptr(), ps, pi, po, py, work.data_ptr(), need, T, K,
                                            M, N, R, r, sb, sx, sy, code, flags))

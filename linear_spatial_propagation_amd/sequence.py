@@ -19,6 +19,8 @@ they were in an ``out`` of the caller's.
 """
 from __future__ import annotations
 
+import functools
+
 from . import _lib
 
 _PACK_SEQ = _lib.packer(_lib.Seq)
@@ -129,18 +131,23 @@ def _gate(gate, x, D, ch_per_weight):
     return _like("gate", gate, x, x.shape if ch_per_weight == 1 else x.shape[:-1] + (D // ch_per_weight,))
 
 
-def _workspace(kept, T, D, N, offsets, ch_per_weight, code, backward, dev):
-    """(pointer, bytes) of a new workspace, which `kept` (a list) keeps until the call is enqueued."""
-    import torch
+@functools.lru_cache(maxsize=4096)
+def _work_bytes(T, D, N, packed, ch_per_weight, code, backward):
     need = _lib.load().gspn_seq_workspace(
-        _PACK_SEQ(0, 0, 0, 0, offsets, 0, 0, 0, 0, 0, 0, T, D, N, 0, 0, 0, 0, 0, ch_per_weight, code, 0), backward)
+        _PACK_SEQ(0, 0, 0, 0, int(packed), 0, 0, 0, 0, 0, 0, T, D, N, 0, 0, 0, 0, 0, ch_per_weight, code, 0), backward)
     if need < 0:
         _lib.check(need)
+    return need
+
+
+def _workspace(T, D, N, packed, ch_per_weight, code, backward, dev):
+    """(tensor, pointer, bytes) of a new workspace; the tensor has to live until the call is enqueued."""
+    import torch
+    need = _work_bytes(T, D, N, packed, ch_per_weight, code, backward)
     if need == 0:
-        return 0, 0
+        return None, 0, 0
     work = torch.empty(need, dtype=torch.uint8, device=dev)
-    kept.append(work)
-    return work.data_ptr(), need
+    return work, work.data_ptr(), need
 
 
 def seq_scan_fwd(x, gate, *, lam=None, u=None, offsets=None, h0=None, ch_per_weight: int = 1, out=None,
@@ -153,7 +160,7 @@ def seq_scan_fwd(x, gate, *, lam=None, u=None, offsets=None, h0=None, ch_per_wei
     """
     import torch
     T, N, D = _sizes(x, ch_per_weight, offsets)
-    dev, code, shape, kept = x.device, _code(x), x.shape, []
+    dev, code, shape = x.device, _code(x), x.shape
     px, sx = x.data_ptr(), _row_stride("x", x)
     pg, sg = _gate(gate, x, D, ch_per_weight)
     pl, sl = _like("lam", lam, x, shape)
@@ -170,7 +177,7 @@ def seq_scan_fwd(x, gate, *, lam=None, u=None, offsets=None, h0=None, ch_per_wei
     if return_states:
         states = torch.empty((lib.gspn_seq_states_rows(T, N, po != 0), D), dtype=torch.float32, device=dev)
         ps = states.data_ptr()
-    pw, nw = _workspace(kept, T, D, N, po, ch_per_weight, code, 0, dev)
+    work, pw, nw = _workspace(T, D, N, po != 0, ch_per_weight, code, 0, dev)
     _call(lib.gspn_seq_fwd, dev, _PACK_SEQ(px, pg, pl, pu, po, ph, py, h_last.data_ptr(), ps, pw, nw, T, D, N, sx, sg,
                                            sl, su, sy, ch_per_weight, code, flags))
     return (out, h_last, states) if return_states else (out, h_last)
@@ -197,7 +204,7 @@ def seq_scan_bwd(x, gate, gy, states, *, lam=None, u=None, offsets=None, gh_last
 def _backward(x, gate, gy, states, lam, u, offsets, gh_last, ch_per_weight, out, want):
     import torch
     T, N, D = _sizes(x, ch_per_weight, offsets)
-    dev, code, shape, kept, lib = x.device, _code(x), x.shape, [], _lib.load()
+    dev, code, shape, lib = x.device, _code(x), x.shape, _lib.load()
     px, sx = x.data_ptr(), _row_stride("x", x)
     pg, sg = _gate(gate, x, D, ch_per_weight)
     pl, sl = _like("lam", lam, x, shape)
@@ -218,7 +225,7 @@ def _backward(x, gate, gy, states, lam, u, offsets, gh_last, ch_per_weight, out,
     gl, tl = _like("glam", out[2], x, shape)
     gu, tu = _like("gu", out[3], x, shape)
     gh = _states("gh0", out[4], dev, (N, D))
-    pw, nw = _workspace(kept, T, D, N, po, ch_per_weight, code, 1, dev)
+    work, pw, nw = _workspace(T, D, N, po != 0, ch_per_weight, code, 1, dev)
     _call(lib.gspn_seq_bwd, dev,
           _PACK_SEQ(px, pg, pl, pu, po, 0, 0, 0, ps, pw, nw, T, D, N, sx, sg, sl, su, 0, ch_per_weight, code, flags),
           _PACK_GRAD(py, ph, gx, gg, gl, gu, gh, sy, tx, tg, tl, tu))
