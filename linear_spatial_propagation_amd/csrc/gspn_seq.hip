@@ -31,8 +31,13 @@
 #include "gspn_kernels.h"
 #include "gspn_rows.h"
 
+#include <type_traits>
+
 namespace gspn {
 namespace {
+
+using Yes = std::integral_constant<bool, true>;
+using No = std::integral_constant<bool, false>;
 
 // ---------------------------------------------------------------- rows
 // V neighbouring channels of a row as they are stored.
@@ -592,7 +597,7 @@ __global__ __launch_bounds__(WAVES * 64) void seq_bwd_kernel(gspn_seq s, gspn_se
         }
         if (la.counters && lane == 0) raise(flag, kHasState);
     }
-    if (count <= 0) return;
+    if (count <= 0 || !valid) return;   // groups of lanes that add up are valid or not as one
     float h[TOKENS + 1][V], G[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -605,61 +610,66 @@ __global__ __launch_bounds__(WAVES * 64) void seq_bwd_kernel(gspn_seq s, gspn_se
         }
     }
     float sum[SHARED ? TOKENS : 1];   // a gate's gradient, of the lane's channels
-    {
+    auto finish = [&](auto whole) {   // WHOLE: all of the wave's tokens, and all gradients
+        constexpr bool WHOLE = decltype(whole)::value;
         const int64_t end = row + count - 1;   // the rows go up from the wave's last
         Walk<T> ox(g.gx, end, g.gx_stride), ol(g.glam, end, g.glam_stride), ou(g.gu, end, g.gu_stride);
         Walk<T> og(g.ggate, end, g.ggate_stride);
 #pragma unroll
         for (int t = TOKENS - 1; t >= 0; --t) {
-            if (t >= count) continue;
-            float vx[V], vl[V], vu[V], vg[V];
+            if (WHOLE || t < count) {
+                float vx[V], vl[V], vu[V], vg[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float a = sg[t][SHARED ? 0 : v];
-                const float x = channel<V>(xv[t], v), small = fabsf(a);
-                G[v] += source(t, v);
-                vx[v] = G[v] * (LAM ? channel<V>(lv[t], v) : take(a, 1.0f + a));
-                vl[v] = G[v] * x;
-                vu[v] = channel<V>(gv[t], v) * h[t + 1][v];
-                vg[v] = fmaf(-small, small, small) * G[v] * (LAM ? h[t][v] : h[t][v] - x);
-                G[v] = keep(a, G[v]);
-            }
-            if (valid) {
-                if (g.gx) put(ox.out(dd), vx);
-                if (LAM && g.glam) put(ol.out(dd), vl);
-                if (U && g.gu) put(ou.out(dd), vu);
-                if (!SHARED && g.ggate) put(og.out(dd), vg);
-            }
-            ox.up(), ol.up(), ou.up(), og.up();
-            if constexpr (SHARED) {
-                sum[t] = vg[0];
-                if constexpr (V == 2) sum[t] += vg[1];
+                for (int v = 0; v < V; ++v) {
+                    const float a = sg[t][SHARED ? 0 : v];
+                    const float x = channel<V>(xv[t], v), small = fabsf(a);
+                    G[v] += source(t, v);
+                    vx[v] = G[v] * (LAM ? channel<V>(lv[t], v) : take(a, 1.0f + a));
+                    vl[v] = G[v] * x;
+                    vu[v] = channel<V>(gv[t], v) * h[t + 1][v];
+                    vg[v] = fmaf(-small, small, small) * G[v] * (LAM ? h[t][v] : h[t][v] - x);
+                    G[v] = keep(a, G[v]);
+                }
+                if (WHOLE || g.gx) put(ox.out(dd), vx);
+                if (LAM && (WHOLE || g.glam)) put(ol.out(dd), vl);
+                if (U && (WHOLE || g.gu)) put(ou.out(dd), vu);
+                if (!SHARED && (WHOLE || g.ggate)) put(og.out(dd), vg);
+                ox.up();
+                if constexpr (LAM) ol.up();
+                if constexpr (U) ou.up();
+                if constexpr (!SHARED) og.up();
+                if constexpr (SHARED) {
+                    sum[t] = vg[0];
+                    if constexpr (V == 2) sum[t] += vg[1];
+                }
             }
         }
-    }
-    if constexpr (SHARED) {
-        if (!g.ggate) return;
-        const int lanes = group / V;   // of a group; its last one ends up with the sum
-        add_lanes(sum, lanes);
-        if (!valid || lane % lanes != lanes - 1) return;
-        if (partial) {
-            const int64_t width = D / group;
-            float* __restrict__ pp = partial + row * width + (uint32_t)d / (uint32_t)group;
+        if constexpr (SHARED) {
+            if (!WHOLE && !g.ggate) return;
+            const int lanes = group / V;   // of a group; its last one ends up with the sum
+            add_lanes(sum, lanes);
+            if (lane % lanes != lanes - 1) return;
+            if (partial) {
+                const int64_t width = D / group;
+                float* __restrict__ pp = partial + row * width + (uint32_t)d / (uint32_t)group;
 #pragma unroll
-            for (int t = 0; t < TOKENS; ++t) {
-                if (t < count) *pp = sum[t];
-                pp += width;
-            }
-        } else {
-            Walk<T> og(g.ggate, row, g.ggate_stride);
+                for (int t = 0; t < TOKENS; ++t) {
+                    if (WHOLE || t < count) *pp = sum[t];
+                    pp += width;
+                }
+            } else {
+                Walk<T> og(g.ggate, row, g.ggate_stride);
 #pragma unroll
-            for (int t = 0; t < TOKENS; ++t) {
-                const float one[1] = {sum[t]};
-                if (t < count) put(og.out(dk), one);
-                og.down();
+                for (int t = 0; t < TOKENS; ++t) {
+                    const float one[1] = {sum[t]};
+                    if (WHOLE || t < count) put(og.out(dk), one);
+                    og.down();
+                }
             }
         }
-    }
+    };
+    if (count == TOKENS && g.gx && g.ggate && (!LAM || g.glam) && (!U || g.gu)) finish(Yes());
+    else finish(No());
 }
 
 // ggate[t][k] = sum of the set's parts, for the rows of sequences.
