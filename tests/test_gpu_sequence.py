@@ -35,29 +35,30 @@ def test_forward_lengths(dtype, lens, D, cpw):
     check(c, call(c))
 
 
-# many tiles behind one another: one sequence, one among single tokens, equal rows
-LONG = [[5003], [1] * 150 + [3001], [2, 0, 2500, 1000, 1]]
+# many tiles behind one another: one sequence, one among single tokens, a few, many of a middling length
+LONG = [[5003], [1] * 150 + [3001], [2, 0, 2500, 1000, 1], [90, 0, 45, 200] * 18]
 
 
-@pytest.mark.parametrize("dtype,D", [("f32", 8), ("bf16", 134)])
+@pytest.mark.parametrize("dtype,D,cpw", [("f32", 8, 2), ("bf16", 134, 2), ("bf16", 35, 5)])
 @pytest.mark.parametrize("lens", LONG, ids=lambda v: f"{len(v)}seq{sum(v)}")
-def test_long_sequences(dtype, D, lens):
+def test_long_sequences(dtype, D, cpw, lens):
     say(f"long {dtype} {len(lens)} sequences, {sum(lens)} tokens, D {D}")
-    c = make(lens, D, dtype=dtype, cpw=2, pad=2, seed=sum(lens))
+    c = make(lens, D, dtype=dtype, cpw=cpw, pad=2, seed=sum(lens))
     check(c, call(c))
     check_grads(c, grads(c))
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("B,L", [(2, 1800), (70, 40)])
-def test_many_equal_rows(dtype, B, L):
+@pytest.mark.parametrize("B,L", [(2, 1800), (70, 40), (8, 530)])
+@pytest.mark.parametrize("D,cpw", [(40, 8), (21, 7)])
+def test_many_equal_rows(dtype, B, L, D, cpw):
     import linear_spatial_propagation_amd as gspn
-    say(f"equal rows {dtype} {B} x {L}, both directions")
-    c = make([L] * B, 40, dtype=dtype, cpw=8, lam=False, seed=B)
+    say(f"equal rows {dtype} {B} x {L}, D {D}, both directions")
+    c = make([L] * B, D, dtype=dtype, cpw=cpw, lam=False, seed=B)
     x, gate, u, gy = (up(c[k]).view(B, L, -1) for k in ("x", "gate", "u", "gy"))
-    y, last, st = gspn.seq_scan_fwd(x, gate, u=u, h0=up(c["h0"]), ch_per_weight=8, return_states=True)
-    check(c, (y.view(B * L, 40), last))
-    g = gspn.seq_scan_bwd(x, gate, gy, st, u=u, gh_last=up(c["gh"]), ch_per_weight=8)
+    y, last, st = gspn.seq_scan_fwd(x, gate, u=u, h0=up(c["h0"]), ch_per_weight=cpw, return_states=True)
+    check(c, (y.view(B * L, D), last))
+    g = gspn.seq_scan_bwd(x, gate, gy, st, u=u, gh_last=up(c["gh"]), ch_per_weight=cpw)
     check_grads(c, [None if t is None else t.reshape(-1, t.shape[-1]) for t in g])
 
 
@@ -110,11 +111,12 @@ def test_repeated_row():
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_gates_at_their_ends(dtype):
-    """Gates of -inf (the state starts over), +inf (it stays), +-200 and 0."""
+    """Gates of -inf (the state starts over), +inf (it stays), the type's lowest and highest, +-200 and 0."""
     c = make([150], 70, dtype=dtype, seed=9)
     g = torch.Generator().manual_seed(1)
-    pick = torch.randint(0, 6, c["gate"].shape, generator=g)
-    for i, v in enumerate((float("-inf"), float("inf"), -200.0, 200.0, 0.0)):
+    pick = torch.randint(0, 8, c["gate"].shape, generator=g)
+    top = torch.finfo(c["gate"].dtype).max
+    for i, v in enumerate((float("-inf"), float("inf"), -top, top, -200.0, 200.0, 0.0)):
         c["gate"][pick == i] = v
     c["lam"] = None
     got = call(c)
@@ -447,6 +449,44 @@ def test_capture_and_replay(cpw):
         float(torch.ones(1 << 16, device="cuda").cumsum(0)[-1])
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_two_graphs():
+    """Two captured calls replayed side by side on two streams: each has a workspace of its own."""
+    cases = [make([900, 300, 1, 0, 400], 160, dtype="bf16", cpw=8, seed=17), make([2000, 3], 96, seed=18)]
+    want = [grads(c) for c in cases]
+    import linear_spatial_propagation_amd as gspn
+    dev = [({k: up(c[k]) for k in ("x", "gate", "lam", "u", "h0", "gy", "gh")}, up(offsets_of(c["lens"]))) for c in cases]
+
+    def once(i):
+        t, off = dev[i]
+        st = gspn.seq_scan_fwd(t["x"], t["gate"], lam=t["lam"], u=t["u"], offsets=off, h0=t["h0"],
+                               ch_per_weight=cases[i]["cpw"], return_states=True)[2]
+        return gspn.seq_scan_bwd(t["x"], t["gate"], t["gy"], st, lam=t["lam"], u=t["u"], offsets=off, gh_last=t["gh"],
+                                 ch_per_weight=cases[i]["cpw"])
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for i in range(2):
+            once(i)
+    torch.cuda.synchronize()
+    graphs, got = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            got.append(once(i))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(4):
+        for g in got:
+            for t in g:
+                t.fill_(7)
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            for a, b in zip(g, w):
+                assert torch.equal(a, b)
 
 
 def test_two_streams():
