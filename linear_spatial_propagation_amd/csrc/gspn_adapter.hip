@@ -210,14 +210,14 @@ struct Launch {
 
 // ---------------------------------------------------------------- shrink
 // RB: blocks of 16 ranks of the workgroup.
-template <typename T, int RB>
-__global__ __launch_bounds__(kWaves * 64, 2) void shrink_kernel(gspn_adapter s, Launch la) {
+template <typename T, int RB, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 2) void shrink_kernel(gspn_adapter s, Launch la) {
     constexpr int kWide = 128 / sizeof(T);          // elements of K of a wave's tile: 128 bytes of a row
     constexpr int kPitch = kWide + 16 / sizeof(T);  // in LDS; 16 bytes more spread the rows over the banks
     constexpr int kPieces = kWide / 8;              // pieces of eight elements of a row
     constexpr int kAtOnce = 64 / kPieces;           // rows of a wave's load
     constexpr int kStage = (kRB + RB) * 16 * kPitch * sizeof(T);   // bytes of LDS of a wave
-    __shared__ __attribute__((aligned(16))) char lds[kWaves * kStage];
+    __shared__ __attribute__((aligned(16))) char lds[WAVES * kStage];
     static_assert(kStage >= kRB * RB * 64 * 16, "the sums take the tiles' place");
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int q = lane >> 4, c = lane & 15;
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void shrink_kernel(gspn_adapter s, 
         la.notes[w] = TileNote{(int32_t)row, count, (int32_t)id, id >= 0 && s.scale ? s.scale[id] : 1.0f};
     if (count == 0 || id < 0) return;
     const int64_t end = ((int64_t)split + 1) * la.slice < s.K ? ((int64_t)split + 1) * la.slice : s.K;
-    f32x4* sums = reinterpret_cast<f32x4*>(lds);    // [kWaves][kRB * RB][64]
+    f32x4* sums = reinterpret_cast<f32x4*>(lds);    // [WAVES][kRB * RB][64]
 
     auto products = [&](auto blocks) {
         constexpr int NB = decltype(blocks)::value;                       // blocks of 16 rows
@@ -273,13 +273,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void shrink_kernel(gspn_adapter s, 
         f32x4 acc[NB][RB] = {};
         int64_t k = (int64_t)split * la.slice + wave * kWide;
         if (k < end) load(k);
-        for (; k < end; k += kWaves * kWide) {
+        for (; k < end; k += WAVES * kWide) {
 #pragma unroll
             for (int i = 0; i < NX; ++i) keep8(xs + (i * kAtOnce + line) * kPitch + 8 * piece, x[i]);
 #pragma unroll
             for (int i = 0; i < NA; ++i) keep8(as + (i * kAtOnce + line) * kPitch + 8 * piece, a[i]);
             handover();
-            if (k + kWaves * kWide < end) load(k + kWaves * kWide);
+            if (k + WAVES * kWide < end) load(k + WAVES * kWide);
 #pragma unroll
             for (int h = 0; h < kWide / 32; ++h) {
                 Frag<T> fa[RB];
@@ -305,12 +305,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void shrink_kernel(gspn_adapter s, 
     else products(std::integral_constant<int, kRB>());
     __syncthreads();
     float* __restrict__ v = la.v + (size_t)split * s.T * la.pitch;
-    for (int b = wave; b < kRB * RB; b += kWaves) {
+    for (int b = wave; b < kRB * RB; b += WAVES) {
         const int t = (b / RB) * 16 + c, i = b % RB;
         if (t >= count) continue;
         f32x4 sum = sums[b * 64 + lane];
 #pragma unroll
-        for (int o = 1; o < kWaves; ++o) sum += sums[(o * kRB * RB + b) * 64 + lane];
+        for (int o = 1; o < WAVES; ++o) sum += sums[(o * kRB * RB + b) * 64 + lane];
         const int64_t j = (int64_t)group * kRanks + i * 16 + 4 * q;
         if (j >= la.pitch) continue;
 #pragma unroll
@@ -329,8 +329,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void shrink_kernel(gspn_adapter s, 
 // The waves of a tile of more than 16 rows have 16 rows each and walk the same
 // columns: each brings a quarter of b's and they share it (two buffers, a
 // barrier a turn).  The waves of up to 16 rows have columns of their own.
+//
+// Two steps in 16 bits fit four workgroups on a CU with five registers put
+// aside (16384 tokens, 4096 columns, r 64: 71 -> 66 us); the others' loops
+// would spill, or fit already.
 template <typename T, int STEPS, int PIECE>
-__global__ __launch_bounds__(kWaves * 64, 2) void expand_kernel(gspn_adapter s, Launch la) {
+__global__ __launch_bounds__(kWaves * 64, STEPS == 2 && PIECE == 8 && sizeof(T) == 2 ? 4 : 2) void expand_kernel(gspn_adapter s, Launch la) {
     constexpr int kSteps = STEPS ? STEPS : sizeof(T) == 2 ? 2 : 1;
     constexpr int kPitch = 32 * kSteps + 16 / sizeof(T);   // of b's rows in LDS
     constexpr int kOPitch = 64 + 4;                        // of a row of sums, fp32
@@ -341,7 +345,6 @@ __global__ __launch_bounds__(kWaves * 64, 2) void expand_kernel(gspn_adapter s, 
     constexpr int kPart = PIECE > 1 ? PIECE : 8;
     constexpr int kOut = 16 * 64 * sizeof(T) / 1024;       // 16-byte pieces of base for a lane
     constexpr int kPer = 16 / sizeof(T);                   // elements of such a piece
-    constexpr int kAhead = 2;                              // turns' worth of base that are on their way
     __shared__ __attribute__((aligned(16))) char lds[kLds];
     typedef typename Piece<T>::x4 Out;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -459,19 +462,17 @@ __global__ __launch_bounds__(kWaves * 64, 2) void expand_kernel(gspn_adapter s, 
                     keep8(bs + lane * kPitch + j, load8(p + j, ranks - j));
             }
         };
-        Out old[kAhead][kOut];
-        auto load_base = [&](int slot, int64_t m) {
-            if (m >= last) return;
+        Out old[kOut];
+        auto load_base = [&](int64_t m) {
 #pragma unroll
             for (int i = 0; i < kOut; ++i) {
                 const int t = i * (64 / kLine) + orow;
                 if (t < mine && m + oc + kPer <= s.M)
-                    old[slot][i] = *reinterpret_cast<const Out*>(base + (row + t) * s.base_stride + m + oc);
+                    old[i] = *reinterpret_cast<const Out*>(base + (row + t) * s.base_stride + m + oc);
             }
         };
         if constexpr (PIECE > 1) load_b(first, 0);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) load_base(i, first + i * stride);
+        if (first < last) load_base(first);
         Parts<T> v[kSteps];
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) v[k] = load_v(k);
@@ -480,11 +481,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void expand_kernel(gspn_adapter s, 
             f32x4 acc[4] = {};
             Out now[kOut];
 #pragma unroll
-            for (int i = 0; i < kOut; ++i) {
-                now[i] = old[0][i];
-#pragma unroll
-                for (int a = 1; a < kAhead; ++a) old[a - 1][i] = old[a][i];
-            }
+            for (int i = 0; i < kOut; ++i) now[i] = old[i];
             const bool more = m + stride < last;
             for (int64_t j0 = 0; j0 < (STEPS ? 1 : s.r); j0 += 32 * kSteps, buffer ^= 1) {
                 T* bs = reinterpret_cast<T*>(lds + (SHARED ? buffer : wave) * kStage);
@@ -496,7 +493,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void expand_kernel(gspn_adapter s, 
                     if (STEPS == 0 && next < s.r) load_b(m, next);
                     else if (more) load_b(m + stride, 0);
                 }
-                if (j0 == 0) load_base(kAhead - 1, m + kAhead * stride);
+                if (j0 == 0 && more) load_base(m + stride);
                 if constexpr (STEPS == 0) {
 #pragma unroll
                     for (int k = 0; k < kSteps; ++k) v[k] = load_v((int)(j0 / 32) + k);
@@ -551,6 +548,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void expand_kernel(gspn_adapter s, 
 }
 
 // ---------------------------------------------------------------- host
+// Waves of a shrink workgroup: eight where a wave's tiles are so large that a CU
+// holds eight at all; then rows with a workgroup for each CU need no splits,
+// which the second launch would read one by one.
+int shrink_waves(const gspn_adapter& s) { return s.r > 32 ? 8 : 4; }
+
 // Sizes of the launches; the workspace holds the tiles' notes and v.
 Launch plan(const gspn_adapter& s) {
     Launch la;
@@ -558,10 +560,11 @@ Launch plan(const gspn_adapter& s) {
     la.total = total_tiles<kRows>(s.offsets, s.T, s.N);
     la.groups = (uint32_t)((s.r + kRanks - 1) / kRanks);
     la.pitch = (s.r + 15) / 16 * 16;
-    // K is shared by more workgroups while there are fewer than two for a CU,
-    // as long as each of their waves has 64 of it
-    const int64_t blocks = (s.K + 63) / 64, most = std::min<int64_t>(kSplits, (blocks + kWaves - 1) / kWaves);
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most, 512 / ((int64_t)la.total * la.groups)));
+    // K is shared by more workgroups while there are fewer than eight waves for a
+    // CU, as long as each has 64 of it
+    const int64_t blocks = (s.K + 63) / 64, waves = shrink_waves(s);
+    const int64_t most = std::min<int64_t>(kSplits, (blocks + waves - 1) / waves);
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most, 2048 / waves / ((int64_t)la.total * la.groups)));
     la.slice = (blocks + want - 1) / want * 64;
     la.splits = (uint32_t)((s.K + la.slice - 1) / la.slice);
     // a workgroup takes up to 1024 columns while workgroups are many
@@ -585,11 +588,11 @@ void expand_pieces(const gspn_adapter& s, F f) {
 template <typename T>
 void launch_typed(const gspn_adapter& s, const Launch& la, hipStream_t stream) {
     const dim3 gs(la.total * la.groups * la.splits), ge(la.total * la.parts);
-    auto shrink = [&](auto kernel) { hipLaunchKernelGGL(kernel, gs, dim3(kWaves * 64), 0, stream, s, la); };
+    auto shrink = [&](auto kernel) { hipLaunchKernelGGL(kernel, gs, dim3(shrink_waves(s) * 64), 0, stream, s, la); };
     auto expand = [&](auto kernel) { hipLaunchKernelGGL(kernel, ge, dim3(kWaves * 64), 0, stream, s, la); };
-    if (s.r <= 16) shrink(shrink_kernel<T, 1>);
-    else if (s.r <= 32) shrink(shrink_kernel<T, 2>);
-    else shrink(shrink_kernel<T, 4>);
+    if (s.r <= 16) shrink(shrink_kernel<T, 1, 4>);
+    else if (s.r <= 32) shrink(shrink_kernel<T, 2, 4>);
+    else shrink(shrink_kernel<T, 4, 8>);
     if (s.r % 8 == 0) expand_pieces<T, 8>(s, expand);
     else if (s.r % 4 == 0) expand_pieces<T, 4>(s, expand);
     else expand_pieces<T, 1>(s, expand);
