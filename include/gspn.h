@@ -398,9 +398,10 @@ int64_t gspn_block_rows(int64_t C_proxy, uint32_t dirs, int32_t ch_per_weight);
  * NULL: N sequences of T / N rows each.  Rows from offsets[N] on belong to
  * no sequence: their inputs are never used and their outputs are left as
  * they were, or set to zero with GSPN_SEQ_ZERO_TAIL.  Values never pass from
- * one sequence to another, NaN and Inf included.  The contents of offsets
- * are not checked; whatever they hold, no access leaves the tensors and the
- * call ends.
+ * one sequence to another, NaN and Inf included (behind an infinite state a
+ * sequence goes on infinite or NaN).  The contents of offsets are not
+ * checked; whatever they hold, no access leaves the tensors and the call
+ * ends.
  *
  * Every x / gate / lam / u / y row starts `*_stride` elements after the one
  * before it (so the four inputs may be column ranges of one projection's
@@ -413,7 +414,9 @@ int64_t gspn_block_rows(int64_t C_proxy, uint32_t dirs, int32_t ch_per_weight);
  *
  * Errors as above: sizes, dtype, pointers, strides, overlaps of an output
  * with anything else the call uses, and the workspace are checked on the
- * host before anything is enqueued.  Calls enqueue on `stream`, allocate
+ * host before anything is enqueued.  A tensor counts from its first element
+ * to its last, so outputs that are column ranges of one buffer, or of an
+ * input's, are refused.  Calls enqueue on `stream`, allocate
  * nothing and keep nothing; results are deterministic.  A workspace is the
  * caller's, 16-byte aligned, needs no initial contents and serves one call
  * at a time: calls that may overlap (two streams, two captured graphs that
@@ -484,7 +487,8 @@ int64_t gspn_seq_states_rows(int64_t T, int64_t N, int32_t packed);
  * s = slots[row] (slots NULL: row), in place.  A row whose slot is outside
  * [0, S) is skipped: it changes no state and its y is left as it was, or set to
  * zero with GSPN_SEQ_ZERO_TAIL (a row of padding takes slot -1).  Rows of the same slot are tokens of one request:
- * they are taken one after the other, in the order of their rows.
+ * they are taken one after the other, in the order of their rows.  Every row
+ * looks through all of slots for them: meant for up to some thousands of rows.
  */
 typedef struct {
     const void *x, *gate, *lam, *u; /* [N][D] ([N][D / ch_per_weight]); lam and u may be NULL */
@@ -506,8 +510,9 @@ int gspn_seq_step(const gspn_seq_token *tok, hipStream_t stream);
  * NULL: T / N rows each).  ids outside [0, R) stand for no adapter: out[t] =
  * base[t].  scale NULL: 1.  out may be base itself (same pointer and stride)
  * and overlaps nothing else.  Rows behind the last request: left as they
- * were, zero with GSPN_SEQ_ZERO_TAIL.  Both products are summed in fp32 and
- * out is rounded once.  1 <= r <= GSPN_MAX_RANK.  Workspace:
+ * were, zero with GSPN_SEQ_ZERO_TAIL.  Both products are summed in fp32, a x
+ * enters the second one with at least 16 bits, and out is rounded once.  b and
+ * scale must be finite: infinities in them may give NaN for the request.  1 <= r <= GSPN_MAX_RANK.  Workspace:
  * gspn_adapter_workspace bytes.
  */
 #define GSPN_MAX_RANK 256

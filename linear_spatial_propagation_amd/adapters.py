@@ -30,7 +30,8 @@ def adapter_add(base, x, a, b, ids, *, scale=None, offsets=None, out=None):
     without offsets every request has T / N of them, and base and x may be
     [N, L, M] and [N, L, K].  float32 or bfloat16, one dtype.  ``out`` may be
     base itself; rows behind the last request are left as they were in an
-    ``out`` of the caller's and zero in a new one.  There is no backward: the
+    ``out`` of the caller's and zero in a new one.  Infinities in b or scale
+    may give NaN for the requests of that adapter.  There is no backward: the
     call refuses tensors that ask for a gradient.
     """
     import torch

@@ -172,7 +172,7 @@ template <> struct Parts<uint16_t> {
     __device__ void set(int e, float v) {
         hi.v[e] = (__bf16)v;
         const float rest = v - (float)hi.v[e];
-        lo.v[e] = (__bf16)(fabsf(v) < __builtin_inff() ? rest : 0.0f);   // an infinite v has no rest
+        lo.v[e] = (__bf16)(fabsf(rest) < __builtin_inff() ? rest : 0.0f);   // an infinity has no rest
     }
 };
 template <> struct Parts<float> {

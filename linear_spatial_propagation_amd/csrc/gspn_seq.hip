@@ -678,13 +678,14 @@ __global__ __launch_bounds__(256) void reduce_gate_kernel(gspn_seq s, gspn_seq_g
                                                           const float* __restrict__ partial) {
     const int64_t sets = s.D / s.ch_per_weight;
     const int parts = s.ch_per_weight / group;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t t = i / sets, k = i - t * sets;
-    if (t >= (s.offsets ? (int64_t)s.offsets[s.N] : s.T) || t >= s.T) return;
-    const float* __restrict__ p = partial + t * (s.D / group) + k * parts;
-    float sum = 0.0f;
-    for (int c = 0; c < parts; ++c) sum += p[c];
-    static_cast<T*>(g.ggate)[t * g.ggate_stride + k] = from_f32(sum, (T*)nullptr);
+    const int64_t given = s.offsets ? (int64_t)s.offsets[s.N] : s.T, rows = given < s.T ? given : s.T;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * sets; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / sets, k = i - t * sets;
+        const float* __restrict__ p = partial + t * (s.D / group) + k * parts;
+        float sum = 0.0f;
+        for (int c = 0; c < parts; ++c) sum += p[c];
+        static_cast<T*>(g.ggate)[t * g.ggate_stride + k] = from_f32(sum, (T*)nullptr);
+    }
 }
 
 // Clears what the tiles tell each other and their counters (a kernel, not a
@@ -934,7 +935,7 @@ void bwd_launch(const gspn_seq& s, const gspn_seq_grad& g, hipStream_t stream) {
     else if (V == 2) bwd_variant<uint16_t, 2, TOKENS, WAVES>(s, go);
     else bwd_variant<uint16_t, 1, TOKENS, WAVES>(s, go);
     if (partial && s.T) {
-        const dim3 grid((unsigned)((s.T * (s.D / s.ch_per_weight) + 255) / 256));
+        const dim3 grid((unsigned)std::min<int64_t>((s.T * (s.D / s.ch_per_weight) + 255) / 256, 4096));
         if (s.dtype == GSPN_BF16)
             hipLaunchKernelGGL(reduce_gate_kernel<uint16_t>, grid, dim3(256), 0, stream, s, g, group, partial);
         else

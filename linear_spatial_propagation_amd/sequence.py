@@ -16,6 +16,10 @@ the cache of seq_step) are float32, [N, D].
 Rows behind offsets[-1] belong to no sequence: nothing of theirs is used, and
 their outputs are zero where this module allocates the output, and left as
 they were in an ``out`` of the caller's.
+
+seq_scan is differentiable; seq_scan_fwd and seq_scan_bwd record nothing for
+autograd.  Workspaces are new for every call, so calls on several streams and
+captured graphs may overlap.
 """
 from __future__ import annotations
 
@@ -278,7 +282,14 @@ _SEQ_SCAN = None
 
 def seq_scan(x, gate, *, lam=None, u=None, offsets=None, h0=None, ch_per_weight: int = 1):
     """seq_scan_fwd as a differentiable torch operation: returns (y, h_last),
-    and autograd calls seq_scan_bwd for the gradients of x, gate, lam, u and h0."""
+    and autograd calls seq_scan_bwd for the gradients of x, gate, lam, u and h0
+    (first derivatives only).
+
+    To capture a training step into a graph, capture seq_scan_fwd and
+    seq_scan_bwd, or a seq_scan with its backward whose leaves have no live
+    graph of an eager call: torch ends the process where a captured backward
+    meets the gradient accumulators of one.
+    """
     import torch
     if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in (x, gate, lam, u, h0)):
         return seq_scan_fwd(x, gate, lam=lam, u=u, offsets=offsets, h0=h0, ch_per_weight=ch_per_weight)
@@ -296,11 +307,15 @@ def seq_step(x, gate, state, *, lam=None, u=None, slots=None, ch_per_weight: int
     each request (None: request n has row n); a request whose slot is outside
     [0, S) is a row of padding, its state stays and its y is left as it was in
     ``out``, zero in a new tensor.  Requests of the same slot are tokens of one
-    request and are taken in order.
+    request and are taken in order (every row looks through all of slots: meant
+    for up to some thousands of requests).  There is no backward: the call
+    refuses tensors that ask for a gradient.
     """
     import torch
     if not x.is_cuda:
         raise ValueError("tensors must be on a GPU (HIP) device")
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, gate, lam, u, state)):
+        raise RuntimeError("seq_step has no backward; call it under torch.no_grad()")
     shape = x.shape
     if len(shape) != 2 or state.dim() != 2:
         raise ValueError("x must be [N, D] and state [S, D]")

@@ -218,6 +218,14 @@ def test_backward_widths(dtype, D, cpw, lam, u):
     check_grads(c, grads(c))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_backward_of_many_shared_gates(dtype):
+    """More gate gradients (2100 x 512) than the launch that adds their parts has lanes."""
+    say(f"backward {dtype} 2100 tokens, 512 gates of 3 channels")
+    c = make([2000, 100], 1536, dtype=dtype, cpw=3, pad=1, seed=77)
+    check_grads(c, grads(c))
+
+
 def test_backward_into_given_tensors_and_strides():
     import linear_spatial_propagation_amd as gspn
     c = make([70, 3, 150], 66, dtype="bf16", cpw=3, pad=4, seed=8)
@@ -365,6 +373,18 @@ def test_step_padding_and_repeated_slots(rows):
         close("state", st, ws, es)
         untouched = torch.tensor([s not in set(slots.tolist()) for s in range(S)])
         assert torch.equal(st.cpu()[untouched], state[untouched])
+
+
+def test_step_refuses_gradients():
+    import linear_spatial_propagation_amd as gspn
+    x, state = torch.ones(2, 8, device="cuda"), torch.zeros(2, 8, device="cuda")
+    gate = torch.zeros(2, 8, device="cuda", requires_grad=True)
+    with pytest.raises(RuntimeError, match="no backward"):
+        gspn.seq_step(x, gate, state)
+    with torch.no_grad():
+        assert torch.equal(gspn.seq_step(x, gate, state), torch.full_like(x, 0.5))
+    # torch.no_grad is not needed for tensors that ask for none
+    gspn.seq_step(x, gate.detach(), state)
 
 
 def test_step_of_no_rows():
