@@ -7,13 +7,21 @@
 //    whose sums stay apart in the workspace.
 //  * expand_kernel: out[t] = base[t] + b[i] (scale[i] sum of the splits' v[t]),
 //    64 columns of 16 rows at a time.
-// Both are matrix products on the matrix cores.  An operand's lanes hold
-// different rows, so loading operands straight from memory asks for 64
-// addresses far apart with every instruction (measured: expand at 2.3 TB/s); so
-// every tile comes in whole row pieces, eight lanes to 128 bytes of a row, and
-// is turned in LDS, and the results go out the same way.  A wave turns its own
-// tiles in LDS of its own: no barriers, and what the next tile needs is loaded
-// while the present one is multiplied.
+// Both are matrix products on the matrix cores, with 2 r operations for every
+// element of x and base: memory bounds them at any rank allowed.  An operand's
+// lanes hold different rows, so loading operands straight from memory asks for 64
+// addresses far apart with every instruction (16384 tokens, 4096 columns, r 64 in
+// bf16: 198 us for both launches); so every tile comes in whole row pieces, eight
+// lanes to 128 bytes of a row, and is turned in LDS, and the results go out the
+// same way.  What the next tile needs is loaded while the present one is multiplied.
+//
+// Measured in bf16 (shrink + expand):
+//   8 requests of 16384 tokens in all, 4096 -> 4096, r 64: 38 + 66 us, where x,
+//   base and out alone are 80 us at a copy's 5.1 TB/s;
+//   64 requests of 2560 tokens (prompts and single tokens), 4096 -> 4096, r 16:
+//   8.5 + 15 to 21 us (the bytes: 14.6); a wave has four turns of 64 columns there,
+//   and the chain of note, v and b in front of the first costs as much as they do;
+//   one token of one request, 1152 -> 1152, r 8: 3.3 + 4.4 us, two empty launches.
 //
 // Rows need not be aligned to 16 bytes: the pieces are read and written at
 // their elements' alignment, which the memory pipeline takes.
@@ -209,7 +217,8 @@ struct Launch {
 };
 
 // ---------------------------------------------------------------- shrink
-// RB: blocks of 16 ranks of the workgroup.
+// RB: blocks of 16 ranks of the workgroup.  A wave turns its own tiles in LDS of
+// its own: no barriers before the waves' sums are added, in a fixed order.
 template <typename T, int RB, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, 2) void shrink_kernel(gspn_adapter s, Launch la) {
     constexpr int kWide = 128 / sizeof(T);          // elements of K of a wave's tile: 128 bytes of a row
@@ -328,7 +337,9 @@ __global__ __launch_bounds__(WAVES * 64, 2) void shrink_kernel(gspn_adapter s, L
 //
 // The waves of a tile of more than 16 rows have 16 rows each and walk the same
 // columns: each brings a quarter of b's and they share it (two buffers, a
-// barrier a turn).  The waves of up to 16 rows have columns of their own.
+// barrier a turn; 86 -> 76 us with it at r 64).  The waves of up to 16 rows have
+// columns of their own.  base is asked for one turn ahead: 70 us; with
+// none ahead 73, with two 72, and more came out slower still.
 //
 // Two steps in 16 bits fit four workgroups on a CU with five registers put
 // aside (16384 tokens, 4096 columns, r 64: 71 -> 66 us); the others' loops
@@ -550,7 +561,8 @@ __global__ __launch_bounds__(kWaves * 64, STEPS == 2 && PIECE == 8 && sizeof(T) 
 // ---------------------------------------------------------------- host
 // Waves of a shrink workgroup: eight where a wave's tiles are so large that a CU
 // holds eight at all; then rows with a workgroup for each CU need no splits,
-// which the second launch would read one by one.
+// which the second launch would read one by one (16384 tokens, r 64: expand 77 -> 72
+// us; 2395 tokens of 27 requests, r 128: 26 -> 21).
 int shrink_waves(const gspn_adapter& s) { return s.r > 32 ? 8 : 4; }
 
 // Sizes of the launches; the workspace holds the tiles' notes and v.
