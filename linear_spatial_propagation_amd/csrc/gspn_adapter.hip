@@ -232,7 +232,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void shrink_kernel(gspn_adapter s, L
     const int q = lane >> 4, c = lane & 15;
     const uint32_t split = blockIdx.x % la.splits, rest = blockIdx.x / la.splits;
     const uint32_t group = rest % la.groups, w = rest / la.groups;
-    const Tile tile = find_tile<kRows>(s.offsets, s.T, s.N, la.tiles, w, lane);
+    const Tile tile = find_tile<kRows>(s.offsets, s.T, s.N, la.tiles, w, lane, first_offsets(s.offsets, s.N, lane));
     const int64_t start = tile.j * kRows;
     const int64_t left = tile.rows - start;
     const int count = uniform((int)(left < 0 ? 0 : left < kRows ? left : kRows));

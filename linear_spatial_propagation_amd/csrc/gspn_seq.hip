@@ -228,20 +228,24 @@ struct Launch {
 
 // How a call's tiles are laid out.  It goes by T, N and the layout alone, as
 // `states` is sized before anything else is known.
-//   kShort: sequences of up to 32 tokens on average, which would leave most waves of
-//           larger tiles without one;
-//   kRows:  many rows of equal length: a tile seldom waits (tile_number), and small
-//           ones let more workgroups into a CU;
-//   kLong:  the rest: the fewer tiles there are in a row, the fewer wait.
-enum Kind { kShort, kRows, kLong };
+//   kShort:  sequences of up to 32 tokens on average, which would leave most waves of
+//            larger tiles without one: tiles of 32;
+//   kMiddle: packed sequences of up to 96 on average: tiles of 64, backward 32 (8192
+//            tokens of 2048 channels in bf16, sequences of 43 on average: 53 and 99
+//            us, with 128 tokens a tile 76 and 153; of 96: 53 and 102, 56 and 112;
+//            of 128: 53 and 104 either way);
+//   kRows:   many rows of equal length: a tile seldom waits (tile_number), and small
+//            ones let more workgroups into a CU;
+//   kLong:   the rest: the fewer tiles there are in a row, the fewer wait.
+enum Kind { kShort, kMiddle, kRows, kLong };
 inline Kind kind_of(int64_t T, int64_t N, bool packed) {
-    return T <= 32 * N ? kShort : !packed && N >= 8 ? kRows : kLong;
+    return T <= 32 * N ? kShort : packed && T <= 96 * N ? kMiddle : !packed && N >= 8 ? kRows : kLong;
 }
 
 // Tokens between two saved states; the backward's tile.
 inline int spacing_of(int64_t T, int64_t N, bool packed) {
     const Kind kind = kind_of(T, N, packed);
-    return kind == kShort ? 32 : kind == kRows ? 64 : 128;
+    return kind <= kMiddle ? 32 : kind == kRows ? 64 : 128;
 }
 
 // The workgroup's tile: from the counter where tiles wait for each other.  Rows of
@@ -277,8 +281,9 @@ __global__ __launch_bounds__(WAVES * 64, 2) void seq_fwd_kernel(gspn_seq s, Laun
     __shared__ int far;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint32_t block = blockIdx.x % la.blocks;
+    const int32_t first_seen = first_offsets(s.offsets, s.N, lane);
     const uint32_t w = tile_number(la, block, false, &number);
-    const Tile tile = find_tile<TILE>(s.offsets, s.T, s.N, la.tiles, w, lane);
+    const Tile tile = find_tile<TILE>(s.offsets, s.T, s.N, la.tiles, w, lane, first_seen);
     const int64_t D = s.D;
     const int64_t d_own = (int64_t)block * (64 * V) + lane * V;
     const bool valid = d_own < D;
@@ -471,8 +476,9 @@ __global__ __launch_bounds__(WAVES * 64) void seq_bwd_kernel(gspn_seq s, gspn_se
     __shared__ int far;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint32_t block = blockIdx.x % la.blocks;
+    const int32_t first_seen = first_offsets(s.offsets, s.N, lane);
     const uint32_t w = tile_number(la, block, true, &number);
-    const Tile tile = find_tile<TILE>(s.offsets, s.T, s.N, la.tiles, w, lane);
+    const Tile tile = find_tile<TILE>(s.offsets, s.T, s.N, la.tiles, w, lane, first_seen);
     const int64_t D = s.D;
     const int64_t d_own = (int64_t)block * (64 * V) + lane * V;
     const bool valid = d_own < D;
@@ -833,7 +839,7 @@ Kind kind_of(const gspn_seq& s) { return kind_of(s.T, s.N, s.offsets != nullptr)
 //   one of 131072, 1024 channels, no lam or u: 220 us with 256, 271 with 128.
 int forward_tile(const gspn_seq& s) {
     const Kind kind = kind_of(s);
-    if (kind != kLong) return spacing_of(s.T, s.N, s.offsets != nullptr);
+    if (kind != kLong) return kind == kShort ? 32 : 64;
     return s.N * ((s.D + 127) / 128) >= 64 ? 128 : 256;
 }
 
@@ -993,7 +999,8 @@ hipError_t launch_seq_fwd(const gspn_seq& s, hipStream_t stream) {
 
 hipError_t launch_seq_bwd(const gspn_seq& s, const gspn_seq_grad& g, hipStream_t stream) {
     switch (kind_of(s)) {
-        case kShort: bwd_launch<8, 4>(s, g, stream); break;
+        case kShort:
+        case kMiddle: bwd_launch<8, 4>(s, g, stream); break;
         case kRows: bwd_launch<8, 8>(s, g, stream); break;
         default: bwd_launch<16, 8>(s, g, stream); break;
     }

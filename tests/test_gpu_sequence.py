@@ -35,6 +35,17 @@ def test_forward_lengths(dtype, lens, D, cpw):
     check(c, call(c))
 
 
+@pytest.mark.parametrize("N", [62, 63, 64, 65, 127, 4095, 4096, 5000])
+def test_numbers_of_sequences(N):
+    """Finding a tile's sequence among 64, 64 x 64 and more, empty ones among them."""
+    say(f"{N} sequences of 0 to 3 tokens and one of 200")
+    lens = [(7 * i + i // 5) % 4 for i in range(N)]
+    lens[N // 3] = 200
+    c = make(lens, 6, dtype="f32", pad=3, seed=N)
+    check(c, call(c))
+    check_grads(c, grads(c))
+
+
 # many tiles behind one another: one sequence, one among single tokens, a few, many of a middling length
 LONG = [[5003], [1] * 150 + [3001], [2, 0, 2500, 1000, 1], [90, 0, 45, 200] * 18]
 
