@@ -5,7 +5,7 @@ from __future__ import annotations
 import functools
 
 from . import _lib
-from .sequence import _call, _code, _index, _layout, _like, _row_stride
+from .sequence import _call, _code, _index, _layout, _like, _new, _row_stride
 
 _PACK = _lib.packer(_lib.Adapter)
 
@@ -69,8 +69,9 @@ def adapter_add(base, x, a, b, ids, *, scale=None, offsets=None, out=None):
         ps = scale.data_ptr()
     flags = 0 if out is not None else _lib.SEQ_ZERO_TAIL
     if out is None:
-        out = torch.empty(base.shape, dtype=x.dtype, device=dev)
-    py, sy = _like("out", out, x, base.shape)
+        out, py, sy = _new(base, M)
+    else:
+        py, sy = _like("out", out, x, base.shape)
     lib = _lib.load()
     need = _work_bytes(T, K, M, N, R, r, code, po != 0)
     work = torch.empty(need, dtype=torch.uint8, device=dev)
