@@ -242,10 +242,17 @@ inline Kind kind_of(int64_t T, int64_t N, bool packed) {
     return T <= 32 * N ? kShort : packed && T <= 96 * N ? kMiddle : !packed && N >= 8 ? kRows : kLong;
 }
 
-// Tokens between two saved states; the backward's tile.
+// Tokens between two saved states; the backward's tile, or half of it.
 inline int spacing_of(int64_t T, int64_t N, bool packed) {
     const Kind kind = kind_of(T, N, packed);
     return kind <= kMiddle ? 32 : kind == kRows ? 64 : 128;
+}
+
+// The row of `states` in front of token `first` of a sequence: sequences take rows
+// as they take tiles of that size (find_tile).
+__device__ __forceinline__ int64_t states_row(const Tile& tile, bool packed, int64_t first, int spacing) {
+    const int64_t per = (tile.rows + spacing - 1) / spacing;
+    return (packed ? tile.row / spacing + tile.n : tile.n * (per > 0 ? per : 1)) + first / spacing;
 }
 
 // The workgroup's tile: from the counter where tiles wait for each other.  Rows of
@@ -400,9 +407,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void seq_fwd_kernel(gspn_seq s, Laun
     for (int v = 0; v < V; ++v) carry[v] = fmaf(pa[v], carry[v], pb[v]);
     const int64_t first = start + wave * TOKENS;
     if (s.states && first % la.spacing == 0 && (first == 0 || first < tile.rows)) {
-        // sequences take rows of `states` as they take tiles (find_tile)
-        const int64_t per = (tile.rows + la.spacing - 1) / la.spacing;
-        const int64_t at = (s.offsets ? tile.row / la.spacing + tile.n : tile.n * (per > 0 ? per : 1)) + first / la.spacing;
+        const int64_t at = states_row(tile, s.offsets != nullptr, first, la.spacing);
 #pragma unroll
         for (int v = 0; v < V; ++v) s.states[at * D + d + v] = carry[v];
     }
@@ -467,7 +472,7 @@ template <int COUNT> __device__ __forceinline__ void add_lanes(float (&v)[COUNT]
 template <typename T, int V, bool SHARED, bool LAM, bool U, int TOKENS, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void seq_bwd_kernel(gspn_seq s, gspn_seq_grad g, Launch la, int group,
                                                              float* __restrict__ partial) {
-    constexpr int TILE = TOKENS * WAVES, WINDOW = 4 * WAVES;   // TILE is the states' spacing
+    constexpr int TILE = TOKENS * WAVES, WINDOW = 4 * WAVES;   // TILE is a multiple of the states' spacing
     using R = typename Raw<T, V>::type;
     using RG = typename Raw<T, SHARED ? 1 : V>::type;
     __shared__ float2 parts[WAVES][V][64], board[WINDOW][V][64];
@@ -582,13 +587,14 @@ __global__ __launch_bounds__(WAVES * 64) void seq_bwd_kernel(gspn_seq s, gspn_se
     {
         float2 f[WAVES][V];
         float e[WAVES][V];
+        const int64_t at = states_row(tile, s.offsets != nullptr, start, la.spacing);
 #pragma unroll
         for (int q = 0; q < WAVES; ++q)
 #pragma unroll
             for (int v = 0; v < V; ++v) f[q][v] = parts[q][v][lane], e[q][v] = back[q][v][lane];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            h0[v] = s.states[(size_t)w * D + d + v];
+            h0[v] = s.states[at * D + d + v];
             pa[v] = 1.0f, pb[v] = 0.0f, ta[v] = 1.0f, tb[v] = 0.0f;
         }
 #pragma unroll
@@ -843,12 +849,16 @@ int forward_tile(const gspn_seq& s) {
     return s.N * ((s.D + 127) / 128) >= 64 ? 128 : 256;
 }
 
-// The backward holds more for a token: at most 128 (the 16 rows: 122 us with
-// tiles of 64, 136 with 128; one row of 32768 tokens of 320 channels in fp32: 70
-// and 55 us).
-int tile_of(const gspn_seq& s, bool backward) {
-    return backward ? spacing_of(s.T, s.N, s.offsets != nullptr) : forward_tile(s);
+// The backward holds more for a token: at most 128.  Rows of equal length with
+// shared gates take 64 (16 rows of 2048, 1152 channels, a gate for 8: 122 us, 136
+// with 128; 32 of 1024, 1024 channels: 130 and 139), with a gate for each channel
+// 128 (12 rows of 704, 2048 channels: 85 us, 97 with 64; 16 of 4096, 512 channels:
+// 157 and 176).
+int backward_tile(const gspn_seq& s) {
+    return kind_of(s) == kRows && s.ch_per_weight == 1 ? 128 : spacing_of(s.T, s.N, s.offsets != nullptr);
 }
+
+int tile_of(const gspn_seq& s, bool backward) { return backward ? backward_tile(s) : forward_tile(s); }
 
 uint32_t tiles_of_sequence(const gspn_seq& s, int tile) {
     const int64_t rows = s.T / s.N;
@@ -998,10 +1008,9 @@ hipError_t launch_seq_fwd(const gspn_seq& s, hipStream_t stream) {
 }
 
 hipError_t launch_seq_bwd(const gspn_seq& s, const gspn_seq_grad& g, hipStream_t stream) {
-    switch (kind_of(s)) {
-        case kShort:
-        case kMiddle: bwd_launch<8, 4>(s, g, stream); break;
-        case kRows: bwd_launch<8, 8>(s, g, stream); break;
+    switch (backward_tile(s)) {
+        case 32: bwd_launch<8, 4>(s, g, stream); break;
+        case 64: bwd_launch<8, 8>(s, g, stream); break;
         default: bwd_launch<16, 8>(s, g, stream); break;
     }
     return hipGetLastError();
