@@ -230,10 +230,10 @@ struct Launch {
 // `states` is sized before anything else is known.
 //   kShort:  sequences of up to 32 tokens on average, which would leave most waves of
 //            larger tiles without one: tiles of 32;
-//   kMiddle: packed sequences of up to 96 on average: tiles of 64, backward 32 (8192
-//            tokens of 2048 channels in bf16, sequences of 43 on average: 53 and 99
-//            us, with 128 tokens a tile 76 and 153; of 96: 53 and 102, 56 and 112;
-//            of 128: 53 and 104 either way);
+//   kMiddle: packed sequences of up to 96 on average: tiles of 64, backward 32 or 64
+//            (8192 tokens of 2048 channels in bf16, a gate for each, sequences of 43
+//            on average: 53 and 99 us, with 128 tokens a tile 76 and 153; of 96: 53
+//            and 102, 56 and 112; of 128: 53 and 104 either way);
 //   kRows:   many rows of equal length: a tile seldom waits (tile_number), and small
 //            ones let more workgroups into a CU;
 //   kLong:   the rest: the fewer tiles there are in a row, the fewer wait.
@@ -242,10 +242,11 @@ inline Kind kind_of(int64_t T, int64_t N, bool packed) {
     return T <= 32 * N ? kShort : packed && T <= 96 * N ? kMiddle : !packed && N >= 8 ? kRows : kLong;
 }
 
-// Tokens between two saved states; the backward's tile, or half of it.
+// Tokens between two saved states, of which the backward's tile is a multiple (64
+// instead of 128 writes 1.5 % more in the forward).
 inline int spacing_of(int64_t T, int64_t N, bool packed) {
     const Kind kind = kind_of(T, N, packed);
-    return kind <= kMiddle ? 32 : kind == kRows ? 64 : 128;
+    return kind <= kMiddle ? 32 : N >= 8 ? 64 : 128;
 }
 
 // The row of `states` in front of token `first` of a sequence: sequences take rows
@@ -849,13 +850,19 @@ int forward_tile(const gspn_seq& s) {
     return s.N * ((s.D + 127) / 128) >= 64 ? 128 : 256;
 }
 
-// The backward holds more for a token: at most 128.  Rows of equal length with
-// shared gates take 64 (16 rows of 2048, 1152 channels, a gate for 8: 122 us, 136
-// with 128; 32 of 1024, 1024 channels: 130 and 139), with a gate for each channel
-// 128 (12 rows of 704, 2048 channels: 85 us, 97 with 64; 16 of 4096, 512 channels:
-// 157 and 176).
+// The backward holds more for a token: at most 128, and a multiple of the spacing.
+// With a gate for each channel 128 (12 equal rows of 704 tokens, 2048 channels in
+// bf16: 85 us, 97 with 64; 16 of 4096, 512 channels: 157 and 176), or 32 where
+// packed sequences are shorter.  Shared gates take less of a tile's registers and 64
+// for all but the shortest and the longest (16 equal rows of 2048, 1152 channels, a
+// gate for 8: 122 us, 136 with 128; 8192 packed tokens, 2048 channels, a gate for
+// 128, sequences of 96 on average: 71 us, 84 with 32; of 200: 68, 78 with 128).
 int backward_tile(const gspn_seq& s) {
-    return kind_of(s) == kRows && s.ch_per_weight == 1 ? 128 : spacing_of(s.T, s.N, s.offsets != nullptr);
+    const Kind kind = kind_of(s);
+    const int spacing = spacing_of(s.T, s.N, s.offsets != nullptr);
+    if (kind == kShort) return 32;
+    if (s.ch_per_weight > 1 && spacing <= 64 && (kind == kRows || s.T <= 512 * s.N)) return 64;
+    return kind == kMiddle ? 32 : 128;
 }
 
 int tile_of(const gspn_seq& s, bool backward) { return backward ? backward_tile(s) : forward_tile(s); }
